@@ -37,6 +37,9 @@ HIP_FLAGS = [
 
 VALU, MFMA32, MFMA16 = 0, 1, 2
 
+# The grouped and 8-bit products (include/grouped_gemm.h), a unit per type.
+RAGGED = ("ragged_api", "ragged_f32", "ragged_bf16", "ragged_f16", "ragged_i8")
+
 
 # Tuples whose kernel (in either variant) the compiler had to spill to
 # scratch memory: written by build() from the compiler's resource report and
@@ -398,6 +401,7 @@ def _build_once(verbose, jobs):
     api = os.path.join(CSRC, "sgemm_api.hip")
     work = [(api, os.path.join(BUILD, "sgemm_api.o"), False),
             (os.path.join(CSRC, "ladder.hip"), os.path.join(BUILD, "ladder.o"), True)]
+    work += [(os.path.join(CSRC, n + ".hip"), os.path.join(BUILD, n + ".o"), True) for n in RAGGED]
     work += [(s, s[:-4] + ".o", True) for s in t_srcs]
     resources = {}
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:

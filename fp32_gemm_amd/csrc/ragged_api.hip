@@ -1,0 +1,309 @@
+// ragged_api.hip -- the C ABI of include/grouped_gemm.h: argument checks, the
+// choice of a tile, and the launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/fp32_gemm.h"
+#include "../../include/grouped_gemm.h"
+#include "ragged_kernels.hpp"
+
+namespace fp32gemm {
+
+hipError_t quantize_launch(int type, const char* x, long long ldx, signed char* q, long long ldq,
+                           float* scale, int M, int K, hipStream_t s);
+void set_last_hip_error(hipError_t e);  // sgemm_api.hip
+
+namespace {
+
+constexpr long long kMaxDim = 1LL << 30, kMaxStride = 1LL << 40, kMaxGroups = 1 << 16;
+constexpr long long kMaxGrid = 0x7FFFFFFFLL;
+constexpr long long kMaxIntegerK = 131071;  // 131071 * 128 * 128 < 2^31
+
+// Bytes of a rows x cols window, and whether two windows share any.
+long long extent(long long rows, long long cols, long long ld, int es) {
+  return rows > 0 && cols > 0 ? ((rows - 1) * ld + cols) * es : 0;
+}
+bool overlap(const void* a, long long an, const void* b, long long bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return an > 0 && bn > 0 && x < y + static_cast<uintptr_t>(bn) && y < x + static_cast<uintptr_t>(an);
+}
+
+bool aligned16(const void* p, long long ld, long long row, long long stride, int es) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0 && row * es % 16 == 0 &&
+         stride * es % 16 == 0;
+}
+
+struct Plan {
+  int shape;
+  int bm, bn;
+  long long grid;
+};
+
+// The tile by the rows a group has on average (the offsets are on the device):
+//   up to 32: 16 x 64, whose waves split the reduction, so that few rows still
+//     keep the weights streaming;
+//   wide (256 x 256) where groups fill such tiles and there are enough of them
+//     for the compute units; else 128 x 128.
+Plan plan(int form, int groups, long long M, long long N, long long K, bool direct) {
+  auto tiles = [](long long n, int t) { return (n + t - 1) / t; };
+  Plan p{};
+  if (form == kFormTN) {
+    const bool wide = direct && groups * tiles(K, 256) * tiles(N, 256) >= 256;
+    p.shape = wide ? kWide : kMid;
+    p.bm = p.bn = wide ? 256 : 128;
+    p.grid = groups * ((tiles(K, p.bm) * tiles(N, p.bn) + 7) / 8 * 8);
+    return p;
+  }
+  const long long used = std::min<long long>(groups, M);
+  // Row tiles: every used group may leave one tile partly filled.
+  auto rows = [&](int bm) { return (M + used * (bm - 1)) / bm; };
+  const long long mean = M / groups;
+  p.shape = mean <= 32 ? kThin : kMid;
+  if (direct && mean >= 384 && rows(256) * tiles(N, 256) >= 200) p.shape = kWide;
+  p.bm = p.shape == kThin ? 16 : p.shape == kMid ? 128 : 256;
+  p.bn = p.shape == kThin ? 64 : p.bm;
+  p.grid = rows(p.bm) * tiles(N, p.bn);
+  return p;
+}
+
+int launch(int type, int form, const RaggedArgs& a, long long M, long long N, long long K, bool direct,
+           void* stream) {
+  const Plan p = plan(form, a.groups, M, N, K, direct);
+  if (p.grid > kMaxGrid) return SGEMM_ERR_UNSUPPORTED;
+  const int rc = sgemm_device_check();
+  if (rc != SGEMM_OK) return rc;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipError_t err = type == kElemF32    ? ragged_f32(form, p.shape, direct, a, p.grid, s)
+                         : type == kElemBF16 ? ragged_bf16(form, p.shape, direct, a, p.grid, s)
+                         : type == kElemF16  ? ragged_f16(form, p.shape, direct, a, p.grid, s)
+                                             : ragged_i8(form, p.shape, direct, a, p.grid, s);
+  if (err != hipSuccess) {
+    set_last_hip_error(err);
+    return SGEMM_ERR_LAUNCH;
+  }
+  return SGEMM_OK;
+}
+
+bool float_type(int t) { return t == GEMM_F32 || t == GEMM_BF16 || t == GEMM_F16; }
+long long at_least(long long n) { return n > 1 ? n : 1; }
+
+// Stores of four elements: rows, the start and the groups aligned to them.
+bool vector_rows(const void* c, long long ldc, long long stride, int es) {
+  return reinterpret_cast<uintptr_t>(c) % (4 * es) == 0 && ldc % 4 == 0 && stride % 4 == 0;
+}
+
+}  // namespace
+}  // namespace fp32gemm
+
+using namespace fp32gemm;
+
+extern "C" {
+
+int gemm_grouped(int32_t type, int32_t out_type, int32_t transpose_w, int32_t groups,
+                 const int32_t* offsets, int64_t M, int64_t N, int64_t K, float alpha, const void* X,
+                 int64_t ldx, const void* W, int64_t ldw, int64_t stride_w, float beta, void* Y,
+                 int64_t ldy, void* stream) {
+  if (!float_type(type)) return -1;
+  if (out_type != type && out_type != GEMM_F32) return -2;
+  if (transpose_w != 0 && transpose_w != 1) return -3;
+  if (groups < 1 || (offsets == nullptr && groups != 1)) return -4;
+  if (M < 0) return -6;
+  if (N < 0) return -7;
+  if (K < 0) return -8;
+  if (X == nullptr && M > 0 && K > 0) return -10;
+  if (ldx < at_least(K)) return -11;
+  if (W == nullptr && N > 0 && K > 0) return -12;
+  if (ldw < at_least(transpose_w ? K : N)) return -13;
+  if (stride_w < 0) return -14;
+  if (Y == nullptr && M > 0 && N > 0) return -16;
+  if (ldy < at_least(N)) return -17;
+  if (M > kMaxDim || N > kMaxDim || K > kMaxDim || ldx >= kRaggedMaxLd || ldw >= kRaggedMaxLd ||
+      ldy >= kRaggedMaxLd || stride_w > kMaxStride || groups > kMaxGroups)
+    return SGEMM_ERR_UNSUPPORTED;
+  const int es = elem_size(type), os = elem_size(out_type);
+  const long long y = extent(M, N, ldy, os);
+  const long long w = extent(transpose_w ? N : K, transpose_w ? K : N, ldw, es);
+  if (overlap(Y, y, X, extent(M, K, ldx, es)) ||
+      overlap(Y, y, W, w ? (groups - 1) * stride_w * es + w : 0) ||
+      (offsets && overlap(Y, y, offsets, 4LL * (groups + 1))))
+    return SGEMM_ERR_OVERLAP;
+  if (M == 0 || N == 0) return SGEMM_OK;
+  RaggedArgs a{};
+  a.A = static_cast<const char*>(X);
+  a.B = static_cast<const char*>(W);
+  a.C = static_cast<char*>(Y);
+  a.offsets = offsets;
+  a.lda = ldx * es;
+  a.ldb = ldw * es;
+  a.ldc = ldy;
+  a.stride_b = stride_w * es;
+  a.groups = groups;
+  a.rows = static_cast<int>(M);
+  a.M = static_cast<int>(M);
+  a.N = static_cast<int>(N);
+  a.K = static_cast<int>(K);
+  a.out = out_type;
+  a.c_vec = vector_rows(Y, ldy, 0, os);
+  a.alpha = alpha;
+  a.beta = beta;
+  const bool direct = aligned16(X, ldx, K, 0, es) && aligned16(W, ldw, transpose_w ? K : N, stride_w, es);
+  return launch(type, transpose_w ? kFormNT : kFormNN, a, M, N, K, direct, stream);
+}
+
+int gemm_grouped_wgrad(int32_t type, int32_t out_type, int32_t groups, const int32_t* offsets,
+                       int64_t M, int64_t N, int64_t K, float alpha, const void* X, int64_t ldx,
+                       const void* dY, int64_t lddy, float beta, void* dW, int64_t lddw,
+                       int64_t stride_dw, void* stream) {
+  if (!float_type(type)) return -1;
+  if (out_type != type && out_type != GEMM_F32) return -2;
+  if (groups < 1 || (offsets == nullptr && groups != 1)) return -3;
+  if (M < 0) return -5;
+  if (N < 0) return -6;
+  if (K < 0) return -7;
+  if (X == nullptr && M > 0 && K > 0) return -9;
+  if (ldx < at_least(K)) return -10;
+  if (dY == nullptr && M > 0 && N > 0) return -11;
+  if (lddy < at_least(N)) return -12;
+  if (dW == nullptr && K > 0 && N > 0) return -14;
+  if (lddw < at_least(N)) return -15;
+  if (M > kMaxDim || N > kMaxDim || K > kMaxDim || ldx >= kRaggedMaxLd || lddy >= kRaggedMaxLd ||
+      lddw >= kRaggedMaxLd || stride_dw > kMaxStride || groups > kMaxGroups)
+    return SGEMM_ERR_UNSUPPORTED;
+  if (stride_dw < 0 || (groups > 1 && K > 0 && N > 0 && stride_dw < (K - 1) * lddw + N)) return -16;
+  const int es = elem_size(type), os = elem_size(out_type);
+  const long long one = extent(K, N, lddw, os), w = one ? (groups - 1) * stride_dw * os + one : 0;
+  if (overlap(dW, w, X, extent(M, K, ldx, es)) || overlap(dW, w, dY, extent(M, N, lddy, es)) ||
+      (offsets && overlap(dW, w, offsets, 4LL * (groups + 1))))
+    return SGEMM_ERR_OVERLAP;
+  if (K == 0 || N == 0) return SGEMM_OK;
+  RaggedArgs a{};
+  a.A = static_cast<const char*>(X);
+  a.B = static_cast<const char*>(dY);
+  a.C = static_cast<char*>(dW);
+  a.offsets = offsets;
+  a.lda = ldx * es;
+  a.ldb = lddy * es;
+  a.ldc = lddw;
+  a.stride_c = stride_dw;
+  a.groups = groups;
+  a.rows = static_cast<int>(M);
+  a.M = static_cast<int>(K);
+  a.N = static_cast<int>(N);
+  a.out = out_type;
+  a.c_vec = vector_rows(dW, lddw, groups > 1 ? stride_dw : 0, os);
+  a.alpha = alpha;
+  a.beta = beta;
+  const bool direct = aligned16(X, ldx, K, 0, es) && aligned16(dY, lddy, N, 0, es);
+  return launch(type, kFormTN, a, M, N, K, direct, stream);
+}
+
+int quantize_rows(int32_t type, int64_t M, int64_t K, const void* X, int64_t ldx, int8_t* Q,
+                  int64_t ldq, float* scale, void* stream) {
+  if (!float_type(type)) return -1;
+  if (M < 0) return -2;
+  if (K < 0) return -3;
+  if (X == nullptr && M > 0 && K > 0) return -4;
+  if (ldx < at_least(K)) return -5;
+  if (Q == nullptr && M > 0 && K > 0) return -6;
+  if (ldq < at_least(K)) return -7;
+  if (scale == nullptr && M > 0) return -8;
+  if (M > kMaxDim || K > kMaxDim || ldx > kMaxDim || ldq > kMaxDim) return SGEMM_ERR_UNSUPPORTED;
+  const long long x = extent(M, K, ldx, elem_size(type)), q = extent(M, K, ldq, 1);
+  if (overlap(Q, q, X, x) || overlap(scale, 4 * M, X, x) || overlap(scale, 4 * M, Q, q))
+    return SGEMM_ERR_OVERLAP;
+  if (M == 0) return SGEMM_OK;
+  const int rc = sgemm_device_check();
+  if (rc != SGEMM_OK) return rc;
+  const hipError_t err =
+      quantize_launch(type, static_cast<const char*>(X), ldx, reinterpret_cast<signed char*>(Q), ldq,
+                      scale, static_cast<int>(M), static_cast<int>(K), static_cast<hipStream_t>(stream));
+  if (err != hipSuccess) {
+    set_last_hip_error(err);
+    return SGEMM_ERR_LAUNCH;
+  }
+  return SGEMM_OK;
+}
+
+int igemm(int32_t out_type, int32_t groups, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
+          const int8_t* A, int64_t lda, const float* scale_a, const int8_t* B, int64_t ldb,
+          int64_t stride_b, const float* scale_b, const float* bias, void* C, int64_t ldc, void* stream) {
+  if (!float_type(out_type)) return -1;
+  if (groups < 1 || (offsets == nullptr && groups != 1)) return -2;
+  if (M < 0) return -4;
+  if (N < 0) return -5;
+  if (K < 0) return -6;
+  if (A == nullptr && M > 0 && K > 0) return -7;
+  if (lda < at_least(K)) return -8;
+  if (scale_a == nullptr && M > 0) return -9;
+  if (B == nullptr && N > 0 && K > 0) return -10;
+  if (ldb < at_least(K)) return -11;
+  if (stride_b < 0) return -12;
+  if (scale_b == nullptr && N > 0) return -13;
+  if (C == nullptr && M > 0 && N > 0) return -15;
+  if (ldc < at_least(N)) return -16;
+  if (M > kMaxDim || N > kMaxDim || K > kMaxIntegerK || lda >= kRaggedMaxLd || ldb >= kRaggedMaxLd ||
+      ldc >= kRaggedMaxLd || stride_b > kMaxStride || groups > kMaxGroups)
+    return SGEMM_ERR_UNSUPPORTED;
+  const long long c = extent(M, N, ldc, elem_size(out_type)), b = extent(N, K, ldb, 1);
+  if (overlap(C, c, A, extent(M, K, lda, 1)) || overlap(C, c, B, b ? (groups - 1) * stride_b + b : 0) ||
+      overlap(C, c, scale_a, 4 * M) || overlap(C, c, scale_b, 4LL * groups * N) ||
+      (bias && overlap(C, c, bias, 4LL * groups * N)) ||
+      (offsets && overlap(C, c, offsets, 4LL * (groups + 1))))
+    return SGEMM_ERR_OVERLAP;
+  if (M == 0 || N == 0) return SGEMM_OK;
+  RaggedArgs a{};
+  a.A = reinterpret_cast<const char*>(A);
+  a.B = reinterpret_cast<const char*>(B);
+  a.C = static_cast<char*>(C);
+  a.offsets = offsets;
+  a.scale_a = scale_a;
+  a.scale_b = scale_b;
+  a.bias = bias;
+  a.lda = lda;
+  a.ldb = ldb;
+  a.ldc = ldc;
+  a.stride_b = stride_b;
+  a.groups = groups;
+  a.rows = static_cast<int>(M);
+  a.M = static_cast<int>(M);
+  a.N = static_cast<int>(N);
+  a.K = static_cast<int>(K);
+  a.out = out_type;
+  a.c_vec = vector_rows(C, ldc, 0, elem_size(out_type));
+  const bool direct = aligned16(A, lda, K, 0, 1) && aligned16(B, ldb, K, stride_b, 1);
+  return launch(kElemI8, kFormNT, a, M, N, K, direct, stream);
+}
+
+int64_t gemm_grouped_plan(int32_t form, int32_t type, int32_t groups, int64_t M, int64_t N, int64_t K,
+                          int32_t aligned, int32_t tile[3]) {
+  if (form < kFormNT || form > kFormTN || type < kElemF32 || type > kElemI8 ||
+      (type == kElemI8 && form != kFormNT) || groups < 1 || groups > kMaxGroups || M < 0 || N < 0 ||
+      K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim || tile == nullptr)
+    return -1;
+  const Plan p = plan(form, groups, M, N, K, aligned != 0);
+  if (p.grid > kMaxGrid) return -1;
+  tile[0] = p.bm;
+  tile[1] = p.bn;
+  tile[2] = aligned != 0;
+  return p.grid;
+}
+
+const char* gemm_grouped_status_string(int status) {
+  static const char* const kArguments[] = {
+      "argument 1 is illegal",  "argument 2 is illegal",  "argument 3 is illegal",
+      "argument 4 is illegal",  "argument 5 is illegal",  "argument 6 is illegal",
+      "argument 7 is illegal",  "argument 8 is illegal",  "argument 9 is illegal",
+      "argument 10 is illegal", "argument 11 is illegal", "argument 12 is illegal",
+      "argument 13 is illegal", "argument 14 is illegal", "argument 15 is illegal",
+      "argument 16 is illegal", "argument 17 is illegal"};
+  if (status < 0 && status >= -17) return kArguments[-status - 1];
+  switch (status) {
+    case SGEMM_ERR_OVERLAP: return "an output overlaps an input";
+    case SGEMM_ERR_UNSUPPORTED: return "size beyond the supported limits";
+    default: return sgemm_status_string(status);
+  }
+}
+
+}  // extern "C"

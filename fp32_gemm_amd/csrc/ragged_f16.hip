@@ -1,0 +1,8 @@
+// ragged_f16.hip -- the grouped products' kernels for f16 operands.
+#include "ragged_float.inc"
+
+namespace fp32gemm {
+hipError_t ragged_f16(int form, int shape, bool direct, const RaggedArgs& a, long long grid, hipStream_t s) {
+  return launch_float<kElemF16>(form, shape, direct, a, grid, s);
+}
+}  // namespace fp32gemm

@@ -758,6 +758,8 @@ int simulate(const Tile& t, int banks, sgemm_sim_report_t* rep) {
 }
 
 }  // namespace
+
+void set_last_hip_error(hipError_t e) { g_last_hip_error = static_cast<int>(e); }  // ragged_api.hip
 }  // namespace fp32gemm
 
 using namespace fp32gemm;
