@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 #include "../../include/fp32_gemm.h"
@@ -30,55 +31,83 @@ bool overlap(const void* a, long long an, const void* b, long long bn) {
   return an > 0 && bn > 0 && x < y + static_cast<uintptr_t>(bn) && y < x + static_cast<uintptr_t>(an);
 }
 
-bool aligned16(const void* p, long long ld, long long row, long long stride, int es) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0 && row * es % 16 == 0 &&
-         stride * es % 16 == 0;
-}
-
 struct Plan {
   int shape;
   int bm, bn;
+  bool longest_first;
   long long grid;
 };
 
-// The tile by the rows a group has on average (the offsets are on the device):
-//   up to 32: 16 x 64, whose waves split the reduction, so that few rows still
-//     keep the weights streaming;
-//   wide (256 x 256) where groups fill such tiles and there are enough of them
-//     for the compute units; else 128 x 128.
-Plan plan(int form, int groups, long long M, long long N, long long K, bool direct) {
+// What a tile costs, in microseconds as measured: a slice of 128 bytes of the
+// reduction on a busy compute unit and on one that holds no other tile, and a
+// tile's start and end with results of 2 and of 4 bytes.  32-bit floats take
+// four times the matrix instructions a slice.
+struct TileCost { double busy, alone, ends2, ends4; };
+constexpr TileCost kCost16[kShapes] = {{1.4, 1.4, 8, 10},   {.50, .64, 2.3, 3}, {.54, .52, 2.3, 3},
+                                       {.19, .28, 1.0, 1.1}, {.135, .2, .5, .5}, {.09, .11, .5, .5}};
+constexpr TileCost kCost32[kShapes] = {{7.1, 7.1, 10, 10},  {1.9, 1.93, 3, 3},   {1.95, 1.93, 3, 3},
+                                       {.53, .62, 1.1, 1.1}, {.14, .22, .5, .5}, {.09, .11, .5, .5}};
+
+// The shape whose tiles, spread over the compute units, are done first by these
+// costs.  The offsets are on the device, so groups are taken as equal but for
+// the last row tile of each, which is half full.
+Plan plan(int form, int type, int out, int groups, long long M, long long N, long long K) {
+  constexpr double kUnits = 256;
   auto tiles = [](long long n, int t) { return (n + t - 1) / t; };
-  Plan p{};
-  if (form == kFormTN) {
-    const bool wide = direct && groups * tiles(K, 256) * tiles(N, 256) >= 256;
-    p.shape = wide ? kWide : kMid;
-    p.bm = p.bn = wide ? 256 : 128;
-    p.grid = groups * ((tiles(K, p.bm) * tiles(N, p.bn) + 7) / 8 * 8);
-    return p;
-  }
   const long long used = std::min<long long>(groups, M);
-  // Row tiles: every used group may leave one tile partly filled.
-  auto rows = [&](int bm) { return (M + used * (bm - 1)) / bm; };
-  const long long mean = M / groups;
-  p.shape = mean <= 32 ? kThin : kMid;
-  if (direct && mean >= 384 && rows(256) * tiles(N, 256) >= 200) p.shape = kWide;
-  p.bm = p.shape == kThin ? 16 : p.shape == kMid ? 128 : 256;
-  p.bn = p.shape == kThin ? 64 : p.bm;
-  p.grid = rows(p.bm) * tiles(N, p.bn);
+  const TileCost* cost = type == kElemF32 ? kCost32 : kCost16;
+  const double steps = form == kFormTN ? static_cast<double>(M) / groups : static_cast<double>(K);
+  const double slices = std::max(1.0, std::ceil(steps * elem_size(type) / 128));
+  Plan p{};
+  double best = 0;
+  for (int shape = 0; shape < kShapes; ++shape) {
+    // Where rows of W are steps, few columns are short pieces of many rows.
+    if ((form == kFormTN && shape == kThin) || (form != kFormNT && shape == kSlim)) continue;
+    const int bm = kRaggedRows[shape], bn = kRaggedCols[shape];
+    const TileCost& c = cost[shape];
+    double count;  // tiles
+    if (form == kFormTN) count = static_cast<double>(groups) * tiles(K, bm) * tiles(N, bn);
+    else if (groups == 1) count = static_cast<double>(tiles(M, bm)) * tiles(N, bn);
+    else if (shape == kWide) count = (static_cast<double>(M) / bm + used / 8.0) * tiles(N, bn);
+    else count = std::max<double>(used, static_cast<double>(M) / bm + used / 2.0) * tiles(N, bn);
+    // Tiles of the fullest compute unit.  Wide ones of ragged groups come in
+    // all sizes and leave some 0.4 of one idle, small ones half of one.
+    double n = count / kUnits;
+    if (shape == kWide && form != kFormTN && groups > 1) n = n <= 1 ? 1 : n + 0.4;
+    else if (shape <= kDeep) n = std::ceil(n);
+    else if (shape == kSmall && n > 1) n += 0.5;
+    const double busy = c.busy * (form == kFormNN && shape == kThin ? 1.5 : 1.0);
+    const double time = std::max(n * busy, c.alone) * slices +
+                        std::max(n, 1.0) * (out == kElemF32 ? c.ends4 : c.ends2);
+    if (best == 0 || time < best) {
+      best = time;
+      p.shape = shape;
+    }
+  }
+  // Looking up the order of the lengths takes some 0.4 us of every tile.
+  p.longest_first = form == kFormTN && slices >= 4;
+  p.bm = kRaggedRows[p.shape];
+  p.bn = kRaggedCols[p.shape];
+  if (form == kFormTN) p.grid = groups * ((tiles(K, p.bm) * tiles(N, p.bn) + 7) / 8 * 8);
+  // Every used group may leave one row tile partly filled; the dies take whole
+  // tiles, and partly filled ones kDeal columns at a time, in eights.
+  else p.grid = (M + used * (p.bm - 1)) / p.bm * tiles(N, p.bn) + used * (kDeal - 1) + 8 + 8 * kDeal;
   return p;
 }
 
-int launch(int type, int form, const RaggedArgs& a, long long M, long long N, long long K, bool direct,
+int launch(int type, int form, const RaggedArgs& a, long long M, long long N, long long K,
            void* stream) {
-  const Plan p = plan(form, a.groups, M, N, K, direct);
+  const Plan p = plan(form, type, a.out, a.groups, M, N, K);
   if (p.grid > kMaxGrid) return SGEMM_ERR_UNSUPPORTED;
+  RaggedArgs args = a;
+  args.longest_first = p.longest_first;
   const int rc = sgemm_device_check();
   if (rc != SGEMM_OK) return rc;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const hipError_t err = type == kElemF32    ? ragged_f32(form, p.shape, direct, a, p.grid, s)
-                         : type == kElemBF16 ? ragged_bf16(form, p.shape, direct, a, p.grid, s)
-                         : type == kElemF16  ? ragged_f16(form, p.shape, direct, a, p.grid, s)
-                                             : ragged_i8(form, p.shape, direct, a, p.grid, s);
+  const hipError_t err = type == kElemF32    ? ragged_f32(form, p.shape, args, p.grid, s)
+                         : type == kElemBF16 ? ragged_bf16(form, p.shape, args, p.grid, s)
+                         : type == kElemF16  ? ragged_f16(form, p.shape, args, p.grid, s)
+                                             : ragged_i8(form, p.shape, args, p.grid, s);
   if (err != hipSuccess) {
     set_last_hip_error(err);
     return SGEMM_ERR_LAUNCH;
@@ -88,11 +117,6 @@ int launch(int type, int form, const RaggedArgs& a, long long M, long long N, lo
 
 bool float_type(int t) { return t == GEMM_F32 || t == GEMM_BF16 || t == GEMM_F16; }
 long long at_least(long long n) { return n > 1 ? n : 1; }
-
-// Stores of four elements: rows, the start and the groups aligned to them.
-bool vector_rows(const void* c, long long ldc, long long stride, int es) {
-  return reinterpret_cast<uintptr_t>(c) % (4 * es) == 0 && ldc % 4 == 0 && stride % 4 == 0;
-}
 
 }  // namespace
 }  // namespace fp32gemm
@@ -145,11 +169,9 @@ int gemm_grouped(int32_t type, int32_t out_type, int32_t transpose_w, int32_t gr
   a.N = static_cast<int>(N);
   a.K = static_cast<int>(K);
   a.out = out_type;
-  a.c_vec = vector_rows(Y, ldy, 0, os);
   a.alpha = alpha;
   a.beta = beta;
-  const bool direct = aligned16(X, ldx, K, 0, es) && aligned16(W, ldw, transpose_w ? K : N, stride_w, es);
-  return launch(type, transpose_w ? kFormNT : kFormNN, a, M, N, K, direct, stream);
+  return launch(type, transpose_w ? kFormNT : kFormNN, a, M, N, K, stream);
 }
 
 int gemm_grouped_wgrad(int32_t type, int32_t out_type, int32_t groups, const int32_t* offsets,
@@ -192,11 +214,9 @@ int gemm_grouped_wgrad(int32_t type, int32_t out_type, int32_t groups, const int
   a.M = static_cast<int>(K);
   a.N = static_cast<int>(N);
   a.out = out_type;
-  a.c_vec = vector_rows(dW, lddw, groups > 1 ? stride_dw : 0, os);
   a.alpha = alpha;
   a.beta = beta;
-  const bool direct = aligned16(X, ldx, K, 0, es) && aligned16(dY, lddy, N, 0, es);
-  return launch(type, kFormTN, a, M, N, K, direct, stream);
+  return launch(type, kFormTN, a, M, N, K, stream);
 }
 
 int quantize_rows(int32_t type, int64_t M, int64_t K, const void* X, int64_t ldx, int8_t* Q,
@@ -271,22 +291,20 @@ int igemm(int32_t out_type, int32_t groups, const int32_t* offsets, int64_t M, i
   a.N = static_cast<int>(N);
   a.K = static_cast<int>(K);
   a.out = out_type;
-  a.c_vec = vector_rows(C, ldc, 0, elem_size(out_type));
-  const bool direct = aligned16(A, lda, K, 0, 1) && aligned16(B, ldb, K, stride_b, 1);
-  return launch(kElemI8, kFormNT, a, M, N, K, direct, stream);
+  return launch(kElemI8, kFormNT, a, M, N, K, stream);
 }
 
-int64_t gemm_grouped_plan(int32_t form, int32_t type, int32_t groups, int64_t M, int64_t N, int64_t K,
-                          int32_t aligned, int32_t tile[3]) {
+int64_t gemm_grouped_plan(int32_t form, int32_t type, int32_t out_type, int32_t groups, int64_t M,
+                          int64_t N, int64_t K, int32_t tile[2]) {
   if (form < kFormNT || form > kFormTN || type < kElemF32 || type > kElemI8 ||
-      (type == kElemI8 && form != kFormNT) || groups < 1 || groups > kMaxGroups || M < 0 || N < 0 ||
-      K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim || tile == nullptr)
+      (type == kElemI8 && form != kFormNT) || !float_type(out_type) || groups < 1 ||
+      groups > kMaxGroups || M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim ||
+      tile == nullptr)
     return -1;
-  const Plan p = plan(form, groups, M, N, K, aligned != 0);
+  const Plan p = plan(form, type, out_type, groups, M, N, K);
   if (p.grid > kMaxGrid) return -1;
   tile[0] = p.bm;
   tile[1] = p.bn;
-  tile[2] = aligned != 0;
   return p.grid;
 }
 

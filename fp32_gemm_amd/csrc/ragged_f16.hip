@@ -2,7 +2,7 @@
 #include "ragged_float.inc"
 
 namespace fp32gemm {
-hipError_t ragged_f16(int form, int shape, bool direct, const RaggedArgs& a, long long grid, hipStream_t s) {
-  return launch_float<kElemF16>(form, shape, direct, a, grid, s);
+hipError_t ragged_f16(int form, int shape, const RaggedArgs& a, long long grid, hipStream_t s) {
+  return launch_float<kElemF16>(form, shape, a, grid, s);
 }
 }  // namespace fp32gemm

@@ -4,13 +4,8 @@
 
 namespace fp32gemm {
 
-hipError_t ragged_i8(int, int shape, bool direct, const RaggedArgs& a, long long grid, hipStream_t s) {
-  if (shape == kThin)
-    return direct ? launch_ragged<kElemI8, kFormNT, RaggedThin>(a, grid, s)
-                  : launch_ragged<kElemI8, kFormNT, RaggedThinAny>(a, grid, s);
-  if (!direct) return launch_ragged<kElemI8, kFormNT, RaggedMidAny>(a, grid, s);
-  return shape == kWide ? launch_ragged<kElemI8, kFormNT, RaggedWide>(a, grid, s)
-                        : launch_ragged<kElemI8, kFormNT, RaggedMid>(a, grid, s);
+hipError_t ragged_i8(int, int shape, const RaggedArgs& a, long long grid, hipStream_t s) {
+  return launch_shape<kElemI8, kFormNT>(shape, a, grid, s);
 }
 
 namespace {

@@ -19,6 +19,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 namespace fp32gemm {
 
@@ -42,29 +43,29 @@ struct RaggedArgs {
   int groups, rows;       // rows: of A (and of B in kFormTN)
   int M, N, K;            // kFormTN: M x N outputs a group; else N columns, K steps
   int out;                // Elem of C
-  int c_vec;              // C's rows allow stores of four elements
+  int longest_first;      // kFormTN: take the groups by falling length
   float alpha, beta;
 };
 
 // A tile of one workgroup: BM x BN outputs, WAVES_M x WAVES_N waves that share
 // each slice, WAVES_K such groups of waves that take every WAVES_K-th slice
-// and add up at the end, S slices in the ring, MF x MF matrix-core blocks.
-// DIRECT: slices go from memory to LDS without passing registers, which takes
-// operands whose rows are whole, aligned 16-byte pieces.
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int WAVES_K_, int S_, int MF_, bool DIRECT_>
+// and add up at the end, S slices of SL bytes in the ring, MF x MF matrix-core blocks,
+// registers for PER_SIMD waves on a SIMD.
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int WAVES_K_, int S_, int SL_, int MF_, int PER_SIMD_>
 struct RaggedTile {
   static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_,
-                       WAVES_K = WAVES_K_, S = DIRECT_ ? S_ : 2, MF = MF_;
-  static constexpr bool DIRECT = DIRECT_;
+                       WAVES_K = WAVES_K_, S = S_, SL = SL_, MF = MF_, PER_SIMD = PER_SIMD_;
   static constexpr int WAVES = WAVES_M * WAVES_N;          // waves of one slice
   static constexpr int NT = WAVES * WAVES_K * 64;
   static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
   static constexpr int FM = WM / MF, FN = WN / MF;         // blocks of a wave
-  static constexpr int STAGE = (BM + BN) * 128;            // bytes of a slice
+  static constexpr int BAND = BM >= 256 ? 4 : 8;           // row tiles that share operands
+  static constexpr int STAGE = (BM + BN) * SL;             // bytes of a slice
   static constexpr int RING = STAGE * S * WAVES_K;
   static constexpr int SUMS = (WAVES_K - 1) * BM * BN * 4; // partial sums at the end
-  static constexpr int LDS = RING > SUMS ? RING : SUMS;
-  static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0, "whole load instructions a wave");
+  static constexpr int OUT = WAVES * MF * (WN + 1) * 4;    // results on their way to memory
+  static constexpr int LDS = RING > SUMS + OUT ? RING : SUMS + OUT;
+  static_assert(BM * SL % (1024 * WAVES) == 0 && BN * SL % (1024 * WAVES) == 0, "whole load instructions a wave");
   static_assert(WM % MF == 0 && WN % MF == 0 && LDS <= 160 * 1024, "tile");
 };
 
@@ -72,6 +73,8 @@ typedef float rf4 __attribute__((ext_vector_type(4)));
 typedef float rf16 __attribute__((ext_vector_type(16)));
 typedef int ri4 __attribute__((ext_vector_type(4)));
 typedef int ri2 __attribute__((ext_vector_type(2)));
+typedef unsigned ru4 __attribute__((ext_vector_type(4)));
+typedef unsigned ru2 __attribute__((ext_vector_type(2)));
 typedef int ri16 __attribute__((ext_vector_type(16)));
 typedef short rs4 __attribute__((ext_vector_type(4)));
 typedef __bf16 rb8 __attribute__((ext_vector_type(8)));
@@ -128,25 +131,29 @@ __device__ __forceinline__ void ragged_mma(Acc& acc, const ri4& b, const ri4& a)
 // Where a slice of one operand lies in LDS.  R: the tile's rows (ALONG: rows
 // are contiguous along the reduction) or columns (rows are reduction steps).
 //
-// ALONG: row r is 128 bytes, its 16-byte piece c at place c ^ (r & 7).  The
-// lanes of a fragment read take the same piece of consecutive rows, which the
-// exclusive or spreads over all banks.
+// The banks are a sweep of 256 bytes, which a cycle of reads covers: sixteen
+// lanes of 16 bytes, 32 of 8 or all 64 of 4.
+// ALONG: row r is 128 bytes, its 16-byte piece c at place c ^ (r / 2 & 7): the
+// lanes of a fragment read take the same piece of consecutive rows, two of
+// which share a sweep.
 // Otherwise: reduction step k is a row of R elements.  Halves are read through
-// the transposing LDS read: sixteen lanes take 4 steps x 32 bytes, so the
-// pieces of step k move by (k & 3) pairs to keep those four rows on different
-// banks; floats are read one by one, the two halves of a wave 4 steps apart,
-// which moves by 128 bytes.
-template <int ELEM, int R, bool ALONG>
+// the transposing LDS read: sixteen lanes take 4 steps x 32 bytes, two such
+// groups a cycle, either 32 bytes (MF 32) or 8 steps (MF 16) apart; the pieces
+// of a step move by 64 bytes for each of the 4 steps and by 32 for the 8.
+// Floats are read one by one, steps 4 (MF 32) or 4, 8 and 12 (MF 16) at once,
+// which move by 128 and 64 bytes.
+template <int ELEM, int R, bool ALONG, int SL>
 struct RaggedSlice {
   static constexpr int ES = elem_size(ELEM);
-  static constexpr int STEPS = 128 / ES;                 // reduction steps of a slice
-  static constexpr int ROW = ALONG ? 128 : R * ES;       // bytes of a row in LDS
+  static constexpr int STEPS = SL / ES;                  // reduction steps of a slice
+  static constexpr int ROW = ALONG ? SL : R * ES;        // bytes of a row in LDS
   static constexpr int PIECES = ROW / 16;
   static constexpr int ROWS_PER_LOAD = 1024 / ROW;       // a wave's load fills 1 KiB
   static __device__ __forceinline__ int swizzle(int row) {
-    if constexpr (ALONG) return row & 7;
-    else if constexpr (ES == 2) return ((row & 3) << 1) & (PIECES - 1);
-    else return ((row & 4) << 1) & (PIECES - 1);
+    if constexpr (ALONG) return SL == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
+    else if constexpr (ES == 2 && ROW >= 256) return (row & 3) << 2 | (row & 8) >> 2;
+    else if constexpr (ES == 2) return ((row & 2) << 1 | (row & 8) >> 2) & (PIECES - 1);
+    else return ((row & 4) << 1 | (row & 8) >> 1) & (PIECES - 1);
   }
   // Row and piece that lane `lane` of load instruction `i` brings.
   static __device__ __forceinline__ int load_row(int i, int lane) {
@@ -157,53 +164,43 @@ struct RaggedSlice {
   }
 };
 
-// Loads of one operand's slices by one wave.  `rows_` and `cols_bytes` bound
-// the operand's window: ALONG, the valid rows of the tile (the reduction's
-// length comes with each slice); otherwise the valid bytes of a step's row.
-template <int ELEM, int R, bool ALONG, int WAVES, bool DIRECT>
+// Loads of one operand's slices by one wave, from memory straight to LDS, 16
+// bytes a lane.  The pieces may start at any byte; a piece that starts in a
+// row's valid part may run past it by up to 15 bytes, which is still inside
+// the operand as long as a later row of at least 16 bytes follows.  Where none
+// does (the last slice, or rows shorter than 16 bytes), and where the part past
+// the end has to read as zero (the end of a reduction), `fetch` and `put` bring
+// the valid bytes and nothing else.
+template <int ELEM, int R, bool ALONG, int SL, int WAVES>
 struct RaggedLoader {
-  using L = RaggedSlice<ELEM, R, ALONG>;
-  static constexpr int NI = R / 8 / WAVES;  // load instructions a wave: R * 128 / 1024 / WAVES
-  static constexpr int LIVE = DIRECT ? 1 : NI;
+  using L = RaggedSlice<ELEM, R, ALONG, SL>;
+  static constexpr int NI = R * SL / 1024 / WAVES;  // load instructions a wave
   const char* base;  // of the next slice
   long long step;    // bytes to the next slice
   int off[NI];       // this lane's bytes past the base, or kRaggedMasked
   int first;         // the wave's first load instruction
-  int lane_;
-  int bound;         // ALONG: bytes from the base to the last valid row's start; else a row's valid bytes
+  int valid;         // ALONG: the tile's valid rows; else the valid bytes of a step's row
   int ld;
-  ri4 reg[LIVE];
-  int more[LIVE];
 
   __device__ __forceinline__ void init(const char* p, long long ld_bytes, long long step_bytes,
-                                       int valid, int wave, int lane) {
+                                       int valid_, int wave, int lane) {
     base = p;
     step = step_bytes;
     ld = static_cast<int>(ld_bytes);
     first = wave * NI;
-    lane_ = lane;
-    bound = ALONG ? (valid - 1) * ld : valid;
+    valid = valid_;
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       const int row = L::load_row(first + j, lane), c = L::load_piece(first + j, lane) * 16;
-      const bool ok = ALONG ? row < valid : c < valid;
-      off[j] = ok ? row * ld + c : kRaggedMasked;
-    }
-  }
-
-  // Masks what lies at or past the reduction's end in this and all later
-  // slices; `left` counts bytes (ALONG) or steps.
-  __device__ __forceinline__ void cut(int left) {
-#pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const int at = ALONG ? L::load_piece(first + j, lane_) * 16 : L::load_row(first + j, lane_);
-      if (at >= left) off[j] = kRaggedMasked;
+      off[j] = (ALONG ? row < valid : c < valid) ? row * ld + c : kRaggedMasked;
     }
   }
 
   // Sends the next slice to `stage` (this operand's part of a ring stage).
-  __device__ __forceinline__ void send(rlds_t stage) {
-    const auto r = ragged_rsrc(base, kRaggedMasked);
+  // Past the reduction's end (`more` false) nothing is fetched, but the
+  // instructions are issued, so that every slice counts the same.
+  __device__ __forceinline__ void send(rlds_t stage, bool more) {
+    const auto r = ragged_rsrc(base, more ? kRaggedMasked : 0);
 #pragma unroll
     for (int j = 0; j < NI; ++j)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -211,79 +208,80 @@ struct RaggedLoader {
     base += step;
   }
 
-  // Without direct loads: fetch the next slice into registers.  Pieces of rows
-  // that start at any byte are covered by whole dwords and shifted into place.
-  // The resource ends with the dword that holds the window's last byte, so no
-  // load leaves the dwords the operand itself lies in.
-  __device__ __forceinline__ void fetch(int left) {
-    const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(base) & 3);
-    const int end = ALONG ? bound + (left < 128 ? left : 128)
-                          : ((left < L::STEPS ? left : L::STEPS) - 1) * ld + bound;
-    const auto r = ragged_rsrc(base - skew, left > 0 ? (end + skew + 3) & ~3 : 0);
+  // Fetches the slice at `p`, of which `left` (bytes ALONG, else steps) exist,
+  // into registers.  A piece with fewer than 16 valid bytes is loaded from the
+  // 16 bytes that end with them, of which some lie among the `ahead` bytes of
+  // the row before p, to be shifted down; `narrow` rows have no 16 bytes and
+  // are put together byte by byte.  Masked buffer loads, not branches, keep all
+  // of them in flight at once.
+  struct Held {
+    ri4 reg[NI];
+    int back[NI];
+  };
+  __device__ __forceinline__ void fetch(Held& h, const char* p, int ahead, int left, bool narrow,
+                                        int lane) const {
+    const auto r = ragged_rsrc(p - ahead, kRaggedMasked);
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
-      const int at = off[j] + skew;
-      reg[j] = __builtin_bit_cast(ri4, __builtin_amdgcn_raw_buffer_load_b128(r, at & ~3, 0, 0));
-      if constexpr (L::ES < 4)
-        more[j] = __builtin_amdgcn_raw_buffer_load_b32(r, (at & 3) ? (at & ~3) + 16 : kRaggedMasked, 0, 0);
+      const int row = L::load_row(first + j, lane), c = L::load_piece(first + j, lane) * 16;
+      const bool ok = ALONG ? row < valid : row < left;
+      const int n = ok ? (ALONG ? left : valid) - c : 0;
+      if (narrow) {
+        const char* q = p + static_cast<long long>(row) * ld + c;
+        unsigned __int128 v = 0;
+        for (int b = 0; b < 16 && b < n; ++b)
+          v |= static_cast<unsigned __int128>(static_cast<unsigned char>(q[b])) << (8 * b);
+        h.reg[j] = __builtin_bit_cast(ri4, v);
+        h.back[j] = 0;
+      } else {
+        h.back[j] = n > 0 && n < 16 ? 16 - n : 0;
+        h.reg[j] = __builtin_bit_cast(
+            ri4, __builtin_amdgcn_raw_buffer_load_b128(
+                     r, n > 0 ? row * ld + ahead + c - h.back[j] : kRaggedMasked, 0, 0));
+      }
     }
   }
-
-  // Writes the fetched slice to `stage` and moves on.
-  __device__ __forceinline__ void put(rlds_t stage, int left) {
-    const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(base) & 3);
+  // Writes the fetched slice to `stage`.
+  __device__ __forceinline__ void put(const Held& h, rlds_t stage, int lane) const {
 #pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      ri4 v = reg[j];
-      if constexpr (L::ES < 4) {
-        const unsigned s = static_cast<unsigned>(off[j] + skew) & 3u;
-        v[0] = __builtin_amdgcn_alignbyte(reg[j][1], reg[j][0], s);
-        v[1] = __builtin_amdgcn_alignbyte(reg[j][2], reg[j][1], s);
-        v[2] = __builtin_amdgcn_alignbyte(reg[j][3], reg[j][2], s);
-        v[3] = __builtin_amdgcn_alignbyte(more[j], reg[j][3], s);
-      }
-      if constexpr (ALONG) {
-        // Bytes past the reduction's end belong to the next row.
-        if (left < 128) {
-          const int valid = left - L::load_piece(first + j, lane_) * 16;
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const int b = valid - 4 * d;
-            v[d] = b >= 4 ? v[d] : b <= 0 ? 0 : v[d] & ((1 << (8 * b)) - 1);
-          }
-        }
-      }
-      *(__attribute__((address_space(3))) ri4*)(stage + (first + j) * 1024 + lane_ * 16) = v;
-    }
-    base += step;
+    for (int j = 0; j < NI; ++j)
+      *(__attribute__((address_space(3))) ri4*)(stage + (first + j) * 1024 + lane * 16) =
+          __builtin_bit_cast(ri4, __builtin_bit_cast(unsigned __int128, h.reg[j]) >> (8 * h.back[j]));
   }
 };
 
-// A lane's 16 operand bytes of block `f` (of the wave's rows or columns that
-// start at `at`) for step group `ks` of a slice.
-template <int ELEM, int R, bool ALONG, int MF>
-__device__ __forceinline__ ri4 ragged_frag(rlds_t stage, int at, int f, int ks, int lane) {
-  using L = RaggedSlice<ELEM, R, ALONG>;
+// The transposing read.  The restricted pointer tells the compiler that the
+// loads to LDS in flight do not write what is read here, which the barrier's
+// explicit wait sees to; without it every read would wait for all of them
+// (grouped product f16 1000 x 1504 x 784 over 8: 24.6 us, with it 16.8).
+typedef __attribute__((address_space(3))) rs4* lds_rs4_t;
+__device__ __forceinline__ ri2 read_transposed(lds_rs4_t __restrict__ p) {
+  return __builtin_bit_cast(ri2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(p));
+}
+
+// A lane's 16 operand bytes of a block whose first row or column is `at`, for
+// step group `ks` of a slice.
+template <int ELEM, int R, bool ALONG, int SL, int MF>
+__device__ __forceinline__ ri4 ragged_frag(rlds_t stage, int at, int ks, int lane) {
+  using L = RaggedSlice<ELEM, R, ALONG, SL>;
   constexpr int GROUPS = 64 / MF;  // 16-byte pieces of the reduction a block takes
   if constexpr (ALONG) {
-    const int row = at + f * MF + lane % MF;
-    const int piece = (ks * GROUPS + lane / MF) ^ (lane & 7);
-    return *(__attribute__((address_space(3))) ri4*)(stage + row * 128 + piece * 16);
+    const int row = at + lane % MF;
+    const int piece = (ks * GROUPS + lane / MF) ^ L::swizzle(lane % MF);
+    return *(__attribute__((address_space(3))) ri4*)(stage + row * SL + piece * 16);
   } else if constexpr (L::ES == 2) {
     // Sixteen lanes read 4 steps x 16 columns (lane s: step s / 4, columns
     // 4 * (s % 4) ..) and each receives one column's four steps.
     const int g = lane / 16, s = lane % 16;
-    const int col = at + f * MF + (MF == 32 ? (g & 1) * 16 : 0) + 4 * (s % 4);
+    const int col = at + (MF == 32 ? (g & 1) * 16 : 0) + 4 * (s % 4);
     const int k = ks * 8 * GROUPS + 8 * (MF == 32 ? g >> 1 : g) + s / 4;
-    const int piece = (col / 8) ^ L::swizzle(s / 4);
+    const int piece = (col / 8) ^ L::swizzle(k);
     rlds_t p = stage + k * L::ROW + piece * 16 + 8 * (s & 1);
-    typedef __attribute__((address_space(3))) rs4* tr_t;
-    const ri2 lo = __builtin_bit_cast(ri2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_t)p));
-    const ri2 hi = __builtin_bit_cast(ri2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_t)(p + 4 * L::ROW)));
+    const ri2 lo = read_transposed((lds_rs4_t)p), hi = read_transposed((lds_rs4_t)(p + 4 * L::ROW));
     return ri4{lo[0], lo[1], hi[0], hi[1]};
   } else {
     ri4 v;
-    const int col = at + f * MF + lane % MF;
+    const int col = at + lane % MF;
     const int k = ks * 4 * GROUPS + 4 * (lane / MF);
     const int piece = (col / 4) ^ L::swizzle(k);
     rlds_t p = stage + k * L::ROW + piece * 16 + 4 * (col & 3);
@@ -293,7 +291,7 @@ __device__ __forceinline__ ri4 ragged_frag(rlds_t stage, int at, int f, int ks, 
   }
 }
 
-// Waits until at most N of the wave's loads are in flight and its LDS reads
+// Waits until at most N of the wave's loads are in flight and its LDS accesses
 // are done, then meets the other waves (ALONE: each wave reads only what it
 // loaded itself).  __syncthreads() would also wait for the N loads.
 template <int N, bool ALONE>
@@ -312,49 +310,15 @@ __device__ __forceinline__ RowSpan group_rows(const RaggedArgs& p, int e) {
   return {lo, min(max(p.offsets[e + 1], lo), p.rows)};
 }
 
-__device__ __forceinline__ int wave_sum_below(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
+// The sum over this and all lower lanes.
+__device__ __forceinline__ int wave_sum_below(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // from 1, 2, 4 and 8 lanes below,
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);  // within rows of sixteen,
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // a row's last lane to the next row,
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // and lane 31 to the upper half
   return v;
-}
-
-// Row tiles of all groups, and the group and row tile of tile `t`.
-template <int BM>
-__device__ __forceinline__ int count_tiles(const RaggedArgs& p, int lane) {
-  if (p.offsets == nullptr) return (p.rows + BM - 1) / BM;
-  int n = 0;
-  for (int e0 = 0; e0 < p.groups; e0 += 64) {
-    if (e0 + lane < p.groups) {
-      const RowSpan s = group_rows(p, e0 + lane);
-      n += (s.hi - s.lo + BM - 1) / BM;
-    }
-  }
-  return __builtin_amdgcn_readlane(wave_sum_below(n, lane), 63);
-}
-
-struct TileAt { int group, tile; };
-template <int BM>
-__device__ __forceinline__ TileAt find_tile(const RaggedArgs& p, int t, int lane) {
-  if (p.offsets == nullptr) return {0, t};
-  int before = 0;
-  for (int e0 = 0; e0 < p.groups; e0 += 64) {
-    int n = 0;
-    if (e0 + lane < p.groups) {
-      const RowSpan s = group_rows(p, e0 + lane);
-      n = (s.hi - s.lo + BM - 1) / BM;
-    }
-    const int upto = before + wave_sum_below(n, lane);
-    const unsigned long long hit = __ballot(upto > t);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
-      return {e0 + l, t - __builtin_amdgcn_readlane(upto - n, l)};
-    }
-    before = __builtin_amdgcn_readlane(upto, 63);
-  }
-  return {-1, 0};
 }
 
 // Consecutive workgroups run on the eight dies in turn, each with its own L2:
@@ -364,90 +328,158 @@ __device__ __forceinline__ int die_order(int w, int tiles) {
   return i < q + (x < r) ? x * q + min(x, r) + i : -1;
 }
 
-// Within a run, tiles go down kBand row tiles before the next column, so that
+// Within a group, tiles go down BAND row tiles before the next column, so that
 // tiles in flight on a die share operand rows and columns in its L2.
-constexpr int kBand = 4;
 struct TileRow { int m, n; };
+template <int BAND>
 __device__ __forceinline__ TileRow band_order(int id, int tm, int tn) {
-  const int band = id / (kBand * tn), first = band * kBand, rows = min(kBand, tm - first);
+  const int band = id / (BAND * tn), first = band * BAND, rows = min(BAND, tm - first);
   const int in = id - first * tn;
   return {first + in % rows, in / rows};
 }
 
-// ---------------------------------------------------------------------------
-// Four neighbouring outputs of row r from column c.
-template <int ELEM, class V4>
-__device__ __forceinline__ void ragged_store(const RaggedArgs& p, long long row, int group, int c,
-                                             const V4& acc, float sa) {
-  if (c >= p.N) return;
-  float v[4];
-  const bool whole = p.c_vec && c + 4 <= p.N;
-  if constexpr (ELEM == kElemI8) {
-    // Sums up to 2^31 are exact; the conversion to 32-bit floats rounds those
-    // past 2^24 once, to half a unit in the last place.
-    const float* sb = p.scale_b + static_cast<long long>(group) * p.N + c;
-    const float* bias = p.bias ? p.bias + static_cast<long long>(group) * p.N + c : nullptr;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (c + i < p.N) v[i] = static_cast<float>(acc[i]) * (sa * sb[i]) + (bias ? bias[i] : 0.0f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = p.alpha * acc[i];
+// The tile of workgroup w: its group, first row, the group's end and its
+// column; group -1 past the last.  Group after group, the last row tile of each
+// partly filled.  A lane counts a group, 64 at a time.
+struct TileAt { int group, row, hi, n; };
+template <int BM, int BAND>
+__device__ __forceinline__ TileAt tile_in_order(const RaggedArgs& p, int w, int tiles_n, int lane) {
+  RowSpan s{0, 0};
+  int before = 0, upto = 0, n = 0, e0 = 0;
+  auto count = [&] {
+    s = e0 + lane < p.groups ? group_rows(p, e0 + lane) : RowSpan{0, 0};
+    n = (s.hi - s.lo + BM - 1) / BM;
+    upto = before + wave_sum_below(n);
+  };
+  for (;; e0 += 64) {
+    count();
+    if (e0 + 64 >= p.groups) break;
+    before = __builtin_amdgcn_readlane(upto, 63);
   }
-  const long long at = row * p.ldc + c;
-  if (p.out == kElemF32) {
-    float* d = reinterpret_cast<float*>(p.C) + at;
-    if (whole) {
-      if (ELEM != kElemI8 && p.beta != 0.0f) {
-        const rf4 o = *reinterpret_cast<const rf4*>(d);
-        for (int i = 0; i < 4; ++i) v[i] += p.beta * o[i];
-      }
-      *reinterpret_cast<rf4*>(d) = rf4{v[0], v[1], v[2], v[3]};
-    } else {
-      for (int i = 0; i < 4; ++i)
-        if (c + i < p.N) d[i] = ELEM != kElemI8 && p.beta != 0.0f ? v[i] + p.beta * d[i] : v[i];
-    }
-  } else if (p.out == kElemBF16) {
-    __bf16* d = reinterpret_cast<__bf16*>(p.C) + at;
-    if (whole) {
-      if (ELEM != kElemI8 && p.beta != 0.0f) {
-        const rb4 o = *reinterpret_cast<const rb4*>(d);
-        for (int i = 0; i < 4; ++i) v[i] += p.beta * static_cast<float>(o[i]);
-      }
-      *reinterpret_cast<rb4*>(d) = rb4{static_cast<__bf16>(v[0]), static_cast<__bf16>(v[1]),
-                                       static_cast<__bf16>(v[2]), static_cast<__bf16>(v[3])};
-    } else {
-      for (int i = 0; i < 4; ++i)
-        if (c + i < p.N)
-          d[i] = static_cast<__bf16>(ELEM != kElemI8 && p.beta != 0.0f
-                                         ? v[i] + p.beta * static_cast<float>(d[i]) : v[i]);
-    }
-  } else {
-    _Float16* d = reinterpret_cast<_Float16*>(p.C) + at;
-    if (whole) {
-      if (ELEM != kElemI8 && p.beta != 0.0f) {
-        const rh4 o = *reinterpret_cast<const rh4*>(d);
-        for (int i = 0; i < 4; ++i) v[i] += p.beta * static_cast<float>(o[i]);
-      }
-      *reinterpret_cast<rh4*>(d) = rh4{static_cast<_Float16>(v[0]), static_cast<_Float16>(v[1]),
-                                       static_cast<_Float16>(v[2]), static_cast<_Float16>(v[3])};
-    } else {
-      for (int i = 0; i < 4; ++i)
-        if (c + i < p.N)
-          d[i] = static_cast<_Float16>(ELEM != kElemI8 && p.beta != 0.0f
-                                           ? v[i] + p.beta * static_cast<float>(d[i]) : v[i]);
+  const int id = die_order(w, __builtin_amdgcn_readlane(upto, 63) * tiles_n);
+  if (id < 0) return {-1, 0, 0, 0};
+  const int want = id / tiles_n;  // the group's row tiles include the want-th of all
+  if (p.groups > 64) {
+    for (e0 = 0, before = 0;; e0 += 64) {
+      count();
+      const int end = __builtin_amdgcn_readlane(upto, 63);
+      if (end > want) break;
+      before = end;
     }
   }
+  const int l = __builtin_ctzll(__ballot(upto > want)), tm = __builtin_amdgcn_readlane(n, l);
+  const TileRow at = band_order<BAND>(id - (__builtin_amdgcn_readlane(upto, l) - tm) * tiles_n, tm, tiles_n);
+  return {e0 + l, __builtin_amdgcn_readlane(s.lo, l) + at.m * BM, __builtin_amdgcn_readlane(s.hi, l), at.n};
 }
 
+// The same for tiles whose time goes by their filled part.  Whole row tiles
+// come first.  The rows that are left of each group make partly filled tiles,
+// which take less time the fewer blocks of CLASS rows they hold; they come
+// last, the fullest first, so that the workgroups that finish early fill up
+// with the short ones.  The dies take them in turn, kDeal columns at a time,
+// which share the rows.
+constexpr int kDeal = 4;
+template <int BM, int CLASS, int BAND>
+__device__ __forceinline__ TileAt tile_by_fill(const RaggedArgs& p, int w, int tiles_n, int lane) {
+  constexpr int NC = BM / CLASS;
+  const int x = w & 7, i = w >> 3;
+  RowSpan s{0, 0};
+  int whole = 0, upto = 0;             // whole row tiles of the lane's group, and of all up to it
+  unsigned long long members[NC];      // groups with c + 1 started blocks left
+  int wholes = 0, parts[NC] = {};      // in the chunks before, and after the first pass in all
+  int e0 = 0;
+  auto count = [&] {
+    s = e0 + lane < p.groups ? group_rows(p, e0 + lane) : RowSpan{0, 0};
+    const int n = s.hi - s.lo, left = (n % BM + CLASS - 1) / CLASS;
+    whole = n / BM;
+    upto = wave_sum_below(whole);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) members[c] = __ballot(left == c + 1);
+  };
+  for (;; e0 += 64) {
+    count();
+    wholes += __builtin_amdgcn_readlane(upto, 63);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) parts[c] += __builtin_popcountll(members[c]);
+    if (e0 + 64 >= p.groups) break;
+  }
+  const int here = wholes * tiles_n / 8 + (x < wholes * tiles_n % 8);  // whole tiles of this die
+  const bool in_whole = i < here;
+  int id, want, n, kind = 0;  // the row tile among the whole ones, or among those of class `kind`
+  if (in_whole) {
+    id = die_order(w, wholes * tiles_n);
+    want = id / tiles_n;
+    n = 0;
+  } else {
+    const int deals = (tiles_n + kDeal - 1) / kDeal;  // of a row tile
+    id = (i - here) / kDeal * 8 + (7 - x);
+    want = id / deals;
+    n = id % deals * kDeal + (i - here) % kDeal;
+    for (kind = NC - 1; kind >= 0; --kind) {
+      int all = 0;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) all = c == kind ? parts[c] : all;
+      if (want < all) break;
+      want -= all;
+    }
+    if (kind < 0 || n >= tiles_n) return {-1, 0, 0, 0};
+  }
+  unsigned long long hit;
+  int before = 0;
+  auto look = [&] {  // the lane whose group holds the tile, counting this chunk's from `before`
+    unsigned long long m = 0;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) m = c == kind ? members[c] : m;
+    const int rank = before + __builtin_amdgcn_mbcnt_hi(
+        static_cast<unsigned>(m >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<unsigned>(m), 0));
+    hit = in_whole ? __ballot(before + upto > want) : __ballot((m >> lane & 1) && rank == want);
+    return in_whole ? __builtin_amdgcn_readlane(upto, 63) : __builtin_popcountll(m);
+  };
+  if (p.groups <= 64) {
+    look();
+  } else {
+    for (e0 = 0;; e0 += 64) {
+      count();
+      const int these = look();
+      if (hit != 0 || e0 + 64 >= p.groups) break;
+      before += these;
+    }
+  }
+  const int l = __builtin_ctzll(hit), tm = __builtin_amdgcn_readlane(whole, l);
+  int row = tm;
+  if (in_whole) {
+    const TileRow at = band_order<BAND>(
+        id - (before + __builtin_amdgcn_readlane(upto, l) - tm) * tiles_n, tm, tiles_n);
+    row = at.m;
+    n = at.n;
+  }
+  return {e0 + l, __builtin_amdgcn_readlane(s.lo, l) + row * BM, __builtin_amdgcn_readlane(s.hi, l), n};
+}
+
+// The group whose length is the `rank`-th largest (the lower one of equals), so
+// that the longest reductions start first.  Past 64 groups: as they come.
+__device__ __forceinline__ int by_length(const RaggedArgs& p, int rank, int lane) {
+  if (p.groups > 64) return rank;
+  const RowSpan s = lane < p.groups ? group_rows(p, lane) : RowSpan{0, -1};
+  const int n = s.hi - s.lo;
+  int above = 0;
+  for (int e = 0; e < p.groups; ++e) {
+    const int o = __builtin_amdgcn_readlane(n, e);
+    above += o > n || (o == n && e < lane);
+  }
+  return __builtin_ctzll(__ballot(lane < p.groups && above == rank));
+}
+
+// ---------------------------------------------------------------------------
 template <int ELEM, int FORM, class T>
-__global__ __launch_bounds__(T::NT, 2) void ragged_kernel(const RaggedArgs p) {
+__global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const RaggedArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the stub alone and lacks the matrix builtins
   constexpr bool A_ALONG = FORM != kFormTN, B_ALONG = FORM == kFormNT;
-  constexpr int ES = elem_size(ELEM), STEPS = 128 / ES, MF = T::MF;
+  constexpr int ES = elem_size(ELEM), SL = T::SL, STEPS = SL / ES, MF = T::MF, S = T::S;
+  constexpr int GROUPS = 64 / MF, KS = SL / 16 / GROUPS;  // step groups of a slice
   using Acc = typename RaggedAcc<ELEM, MF>::type;
-  using LoadA = RaggedLoader<ELEM, T::BM, A_ALONG, T::WAVES, T::DIRECT>;
-  using LoadB = RaggedLoader<ELEM, T::BN, B_ALONG, T::WAVES, T::DIRECT>;
+  using LoadA = RaggedLoader<ELEM, T::BM, A_ALONG, SL, T::WAVES>;
+  using LoadB = RaggedLoader<ELEM, T::BN, B_ALONG, SL, T::WAVES>;
   __shared__ __attribute__((aligned(1024))) char lds[T::LDS];
 
   const int lane = threadIdx.x & 63;
@@ -456,19 +488,21 @@ __global__ __launch_bounds__(T::NT, 2) void ragged_kernel(const RaggedArgs p) {
   const int tiles_n = (p.N + T::BN - 1) / T::BN;
 
   // The tile: its group, its window of A, B and C, and the reduction's length.
-  int group, m0, rows, len;
+  int group, rows, len;
   long long row_c;
   const char *a, *b;
-  int n0;
+  int n0, m_bytes = 0;  // the tile's first column of B, and byte of a step's row of A
   if constexpr (FORM == kFormTN) {
     // Each group's tiles are dealt out over all dies: groups differ in length.
     const int tiles_m = (p.M + T::BM - 1) / T::BM, each = tiles_m * tiles_n, room = (each + 7) & ~7;
     group = blockIdx.x / room;
+    if (p.longest_first) group = by_length(p, group, lane);
     const int id = die_order(blockIdx.x % room, each);
     if (id < 0) return;
-    const TileRow at = band_order(id, tiles_m, tiles_n);
+    const TileRow at = band_order<T::BAND>(id, tiles_m, tiles_n);
     const RowSpan s = group_rows(p, group);
-    m0 = at.m * T::BM;
+    const int m0 = at.m * T::BM;
+    m_bytes = m0 * ES;
     n0 = at.n * T::BN;
     rows = min(T::BM, p.M - m0);
     len = s.hi - s.lo;
@@ -476,39 +510,46 @@ __global__ __launch_bounds__(T::NT, 2) void ragged_kernel(const RaggedArgs p) {
     b = p.B + s.lo * p.ldb + static_cast<long long>(n0) * ES;
     row_c = m0;
   } else {
-    const int tiles_m = count_tiles<T::BM>(p, lane);
-    const int id = die_order(blockIdx.x, tiles_m * tiles_n);
-    if (id < 0) return;
-    const TileRow at = band_order(id, tiles_m, tiles_n);
-    const TileAt where = find_tile<T::BM>(p, at.m, lane);
-    group = where.group;
+    TileAt at;
+    if constexpr (T::FM == 4) at = tile_by_fill<T::BM, T::BM / 4, T::BAND>(p, blockIdx.x, tiles_n, lane);
+    else at = tile_in_order<T::BM, T::BAND>(p, blockIdx.x, tiles_n, lane);
+    group = at.group;
     if (group < 0) return;
-    const RowSpan s = group_rows(p, group);
-    m0 = s.lo + where.tile * T::BM;
     n0 = at.n * T::BN;
-    rows = min(T::BM, s.hi - m0);
+    rows = min(T::BM, at.hi - at.row);
     len = p.K;
-    a = p.A + m0 * p.lda;
+    a = p.A + at.row * p.lda;
     b = p.B + group * p.stride_b + (B_ALONG ? n0 * p.ldb : static_cast<long long>(n0) * ES);
-    row_c = m0;
+    row_c = at.row;
   }
   const int cols = min(T::BN, p.N - n0);
 
-  const int slices = (len + STEPS - 1) / STEPS, turns = (slices + T::WAVES_K - 1) / T::WAVES_K;
+  // Slice 0 is the one that goes through registers, if there is one: what is
+  // left of the reduction after whole slices, or the last whole slice where
+  // rows that are steps end inside a piece.  The others follow in order; group
+  // g of waves takes slices g, g + WAVES_K, ...
+  const bool cross = (!A_ALONG && rows * ES % 16 != 0) || (!B_ALONG && cols * ES % 16 != 0);
+  const int over = len % STEPS, head = over ? over : cross && len > 0 ? STEPS : 0;
+  const int whole = (len - head) / STEPS, slices = whole + (head > 0);
+  const int turns = (slices + T::WAVES_K - 1) / T::WAVES_K;
+  const bool narrow_a = A_ALONG ? len * ES < 16 : p.M * ES < 16;
+  const bool narrow_b = B_ALONG ? len * ES < 16 : p.N * ES < 16;
   LoadA la;
   LoadB lb;
-  {
-    const long long sa = A_ALONG ? 128 : STEPS * p.lda, sb = B_ALONG ? 128 : STEPS * p.ldb;
-    la.init(a + kgroup * sa, p.lda, sa * T::WAVES_K, A_ALONG ? rows : rows * ES, wave, lane);
-    lb.init(b + kgroup * sb, p.ldb, sb * T::WAVES_K, B_ALONG ? cols : cols * ES, wave, lane);
-  }
-  const rlds_t ring = (rlds_t)lds + kgroup * (T::STAGE * T::S);
-  int left = len - kgroup * STEPS;  // reduction steps from the next slice to load
-  auto cut = [&] {
-    if (left < STEPS) {
-      la.cut(A_ALONG ? left * ES : left);
-      lb.cut(B_ALONG ? left * ES : left);
-    }
+  const long long sa = A_ALONG ? SL : STEPS * p.lda, sb = B_ALONG ? SL : STEPS * p.ldb;
+  const int skip = kgroup - (head > 0);  // whole slices before this group's first (-1: starts at slice 0)
+  la.init(a + skip * sa, p.lda, sa * T::WAVES_K, A_ALONG ? rows : rows * ES, wave, lane);
+  lb.init(b + skip * sb, p.ldb, sb * T::WAVES_K, B_ALONG ? cols : cols * ES, wave, lane);
+  int left_a = whole - skip, left_b = left_a;  // whole slices from the next on (and slice 0, of group 0)
+  const rlds_t ring = (rlds_t)lds + kgroup * (T::STAGE * S);
+
+  auto send_a = [&](int stage) {
+    la.send(ring + stage * T::STAGE, left_a > 0);
+    left_a -= T::WAVES_K;
+  };
+  auto send_b = [&](int stage) {
+    lb.send(ring + stage * T::STAGE + T::BM * SL, left_b > 0);
+    left_b -= T::WAVES_K;
   };
 
   Acc acc[T::FM][T::FN];
@@ -517,77 +558,175 @@ __global__ __launch_bounds__(T::NT, 2) void ragged_kernel(const RaggedArgs p) {
 #pragma unroll
     for (int j = 0; j < T::FN; ++j) acc[i][j] = Acc{};
 
-  const int am = (wave / T::WAVES_N) * T::WM, bn = (wave % T::WAVES_N) * T::WN;
-  auto multiply = [&](rlds_t stage) {
-    constexpr int GROUPS = 64 / MF, KS = 8 / GROUPS;
+  // The waves of a tile's rows take its blocks of MF rows in turn, so that in a
+  // partly filled tile they have the same number of blocks to leave out.
+  const int wave_m = wave / T::WAVES_N, bn = (wave % T::WAVES_N) * T::WN;
+  constexpr int MSTEP = T::WAVES_M * MF;
+  auto block_row = [&](int i) { return i * MSTEP + wave_m * MF; };
+
+  // Scales and biases of 8-bit products are fetched ahead, from clamped places
+  // where the tile ends: a lane's four columns, and a row of each block.
+  constexpr int PIECES = T::WN / 4;  // of four columns
+  const int cn = n0 + bn;            // the wave's first column
+  const int c4 = lane % PIECES, n4 = cn + 4 * c4;
+  const float* const sb_row = ELEM == kElemI8 ? p.scale_b + static_cast<long long>(group) * p.N : nullptr;
+  const float* const bias_row =
+      ELEM == kElemI8 && p.bias ? p.bias + static_cast<long long>(group) * p.N : nullptr;
+  float sb4[4] = {}, bias4[4] = {}, scale_m[T::FM] = {};
+  if constexpr (ELEM == kElemI8) {
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      ri4 fa[T::FM], fb[T::FN];
+    for (int i = 0; i < 4; ++i) sb4[i] = sb_row[min(n4 + i, p.N - 1)];
+    if (bias_row)
 #pragma unroll
-      for (int i = 0; i < T::FM; ++i)
-        fa[i] = ragged_frag<ELEM, T::BM, A_ALONG, MF>(stage, am, i, ks, lane);
+      for (int i = 0; i < 4; ++i) bias4[i] = bias_row[min(n4 + i, p.N - 1)];
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i)
+      scale_m[i] = p.scale_a[row_c + min(block_row(i) + lane % MF, rows - 1)];
+  }
+
+  auto run = [&](auto blocks) {
+    constexpr int NF = decltype(blocks)::value;  // row blocks a wave multiplies
+    constexpr bool ALONE = T::WAVES == 1;
+    constexpr int NIA = LoadA::NI, NIB = LoadB::NI;
+    ri4 fa[2][NF], fb[2][T::FN];
+    auto read = [&](int half, rlds_t stage, int ks) {
+#pragma unroll
+      for (int i = 0; i < NF; ++i)
+        fa[half][i] = ragged_frag<ELEM, T::BM, A_ALONG, SL, MF>(stage, block_row(i), ks, lane);
 #pragma unroll
       for (int j = 0; j < T::FN; ++j)
-        fb[j] = ragged_frag<ELEM, T::BN, B_ALONG, MF>(stage + T::BM * 128, bn, j, ks, lane);
+        fb[half][j] = ragged_frag<ELEM, T::BN, B_ALONG, SL, MF>(stage + T::BM * SL, bn + j * MF, ks, lane);
+    };
+    // Order within a step group: the next group's reads and the loads go
+    // between the matrix instructions.
+    auto schedule = [&](auto loads) {
+      constexpr int NM = NF * T::FN * (ELEM == kElemF32 ? 4 : 1), NL = decltype(loads)::value;
+      constexpr int RA = A_ALONG ? 1 : ES == 2 ? 2 : 4, RB = B_ALONG ? 1 : ES == 2 ? 2 : 4;
+      constexpr int ND = NF * RA + T::FN * RB;
+      // The loads write LDS, so they stay behind the reads: reads go in the
+      // first part of the group, loads in the second.
+      constexpr int DPART = NL ? (NM * ND + ND + NL - 1) / (ND + NL) : NM, LPART = NM - DPART;
+      constexpr int DEACH = (ND + DPART - 1) / DPART, LEACH = LPART > 0 ? (NL + LPART - 1) / LPART : NL;
 #pragma unroll
-      for (int i = 0; i < T::FM; ++i)
+      for (int i = 0; i < NM; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (i * DEACH < ND) __builtin_amdgcn_sched_group_barrier(0x100, DEACH, 0);
+        else if (NL > 0) __builtin_amdgcn_sched_group_barrier(0x020, LEACH, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    ragged_barrier<(S - 2) * (NIA + NIB) + NIA, ALONE>();
+    read(0, ring, 0);
+    int at = 0;
+    // Step group ks of the slice in stage `at` is multiplied from one half of
+    // the operand registers while the next one is read to the other half.
+    auto step_group = [&](auto group) {
+      constexpr int ks = decltype(group)::value, half = ks & 1;
+      // The stage's last reads are done before the barrier, so behind it the
+      // slice S turns on may take its place, and the next slice is there.
+      if constexpr (ks == KS - 1) {
+        ragged_barrier<(S - 2) * (NIA + NIB), ALONE>();
+        __builtin_amdgcn_sched_barrier(0);
+        read(0, ring + (at + 1 == S ? 0 : at + 1) * T::STAGE, 0);
+        send_a(at);
+      } else {
+        read(1 - half, ring + at * T::STAGE, ks + 1);
+        if constexpr (ks == 0) send_b(at == 0 ? S - 1 : at - 1);
+      }
+      // Dense bf16 8192 x 8192 x 8192 with transposed weights: 824 us without
+      // the priority, 794 with it; with plain weights no better (897, 917).
+      if constexpr (FORM == kFormNT) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int j = 0; j < T::FN; ++j) ragged_mma<ELEM, MF>(acc[i][j], fb[j], fa[i]);
+      for (int i = 0; i < NF; ++i)
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j) ragged_mma<ELEM, MF>(acc[i][j], fb[half][j], fa[half][i]);
+      if constexpr (FORM == kFormNT) __builtin_amdgcn_s_setprio(0);
+      schedule(std::integral_constant<int, (ks == KS - 1 ? NIA : ks == 0 ? NIB : 0)>{});
+    };
+    for (int t = 0; t < turns; ++t) {
+      step_group(std::integral_constant<int, 0>{});
+      step_group(std::integral_constant<int, 1>{});
+      if constexpr (KS == 4) {
+        step_group(std::integral_constant<int, 2>{});
+        step_group(std::integral_constant<int, 3>{});
+      }
+      at = at + 1 == S ? 0 : at + 1;
     }
   };
 
-  constexpr bool ALONE = T::WAVES == 1;
-  if constexpr (T::DIRECT) {
-    constexpr int NI = LoadA::NI + LoadB::NI;
-    auto send = [&](int stage) {
-      cut();
-      la.send(ring + stage * T::STAGE);
-      lb.send(ring + stage * T::STAGE + T::BM * 128);
-      left -= STEPS * T::WAVES_K;
-    };
-#pragma unroll
-    for (int s = 0; s < T::S - 1; ++s) send(s);
-    int at = 0, next = T::S - 1;
+  // A slice through registers: `left` steps of the reduction from step `done`.
+  auto place = [&](int done, int left) {
+    typename LoadA::Held ha;
+    typename LoadB::Held hb;
+    if constexpr (A_ALONG) la.fetch(ha, a + done * ES, done * ES, left * ES, narrow_a, lane);
+    else la.fetch(ha, a + done * p.lda, m_bytes, left, narrow_a, lane);
+    if constexpr (B_ALONG) lb.fetch(hb, b + done * ES, done * ES, left * ES, narrow_b, lane);
+    else lb.fetch(hb, b + done * p.ldb, n0 * ES, left, narrow_b, lane);
+    la.put(ha, ring, lane);
+    lb.put(hb, ring + T::BM * SL, lane);
+  };
+
+  // Rows of fewer than 16 bytes that are reduction steps: every slice goes
+  // through registers.
+  auto run_narrow = [&] {
     for (int t = 0; t < turns; ++t) {
-      ragged_barrier<(T::S - 2) * NI, ALONE>();
-      send(next);
-      multiply(ring + at * T::STAGE);
-      at = at + 1 == T::S ? 0 : at + 1;
-      next = next + 1 == T::S ? 0 : next + 1;
-    }
-    // The slices past the end, all masked, may still be on their way to LDS.
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  } else {
-    auto fetch = [&] {
-      cut();
-      la.fetch(A_ALONG ? left * ES : left);
-      lb.fetch(B_ALONG ? left * ES : left);
-    };
-    auto put = [&](int stage) {
-      la.put(ring + stage * T::STAGE, A_ALONG ? left * ES : left);
-      lb.put(ring + stage * T::STAGE + T::BM * 128, B_ALONG ? left * ES : left);
-      left -= STEPS * T::WAVES_K;
-    };
-    if (turns > 0) {
-      fetch();
-      put(0);
-    }
-    for (int t = 0; t < turns; ++t) {
+      const int done = (t * T::WAVES_K + kgroup) * STEPS;
+      place(done, min(STEPS, len - done));
       __syncthreads();
-      if (t + 1 < turns) fetch();
-      multiply(ring + (t & 1) * T::STAGE);
-      if (t + 1 < turns) put((t + 1) & 1);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i) {
+          const ri4 fa = ragged_frag<ELEM, T::BM, A_ALONG, SL, MF>(ring, block_row(i), ks, lane);
+#pragma unroll
+          for (int j = 0; j < T::FN; ++j)
+            ragged_mma<ELEM, MF>(
+                acc[i][j], ragged_frag<ELEM, T::BN, B_ALONG, SL, MF>(ring + T::BM * SL, bn + j * MF, ks, lane), fa);
+        }
+      __syncthreads();
+    }
+  };
+
+  if (FORM != kFormNT && ((!A_ALONG && narrow_a) || (!B_ALONG && narrow_b))) {
+    if constexpr (FORM != kFormNT) run_narrow();
+  } else {
+    // The first S slices are sent ahead (the last one's B in the first group).
+    const bool headed = head > 0 && kgroup == 0;
+    if (headed) {
+      la.base += la.step;
+      lb.base += lb.step;
+      left_a -= T::WAVES_K;
+      left_b -= T::WAVES_K;
+    } else {
+      send_a(0);
+      send_b(0);
+    }
+#pragma unroll
+    for (int s = 1; s < S; ++s) {
+      send_a(s);
+      if (s < S - 1) send_b(s);
+    }
+    if (headed) place(len - head, head);
+    if constexpr (FORM != kFormTN && T::FM == 4) {
+      const int used = (rows - wave_m * MF + MSTEP - 1) / MSTEP;
+      if (used > 3) run(std::integral_constant<int, 4>{});
+      else if (used == 3) run(std::integral_constant<int, 3>{});
+      else if (used == 2) run(std::integral_constant<int, 2>{});
+      else run(std::integral_constant<int, 1>{});
+    } else {
+      run(std::integral_constant<int, T::FM>{});
     }
   }
+  // The slices past the end, which hold nothing, may still be on their way.
+  ragged_barrier<0, false>();
 
   // Wave groups that took other slices hand over their sums, in a fixed order.
   constexpr int REGS = MF * MF / 64;
   if constexpr (T::WAVES_K > 1) {
-    using S = decltype(acc[0][0][0] + acc[0][0][0]);
-    __attribute__((address_space(3))) S* sums = (__attribute__((address_space(3))) S*)(rlds_t)lds;
+    using V = decltype(acc[0][0][0] + acc[0][0][0]);
+    __attribute__((address_space(3))) V* sums = (__attribute__((address_space(3))) V*)(rlds_t)lds;
     const int slot = wave * 64 + lane;
     constexpr int EACH = T::WAVES * 64;
-    __syncthreads();
     if (kgroup > 0) {
 #pragma unroll
       for (int i = 0; i < T::FM; ++i)
@@ -610,23 +749,126 @@ __global__ __launch_bounds__(T::NT, 2) void ragged_kernel(const RaggedArgs p) {
             acc[i][j][r] += sums[(((g * T::FM + i) * T::FN + j) * REGS + r) * EACH + slot];
   }
 
-  RaggedArgs q = p;
-  if constexpr (FORM == kFormTN)
-    q.C += group * p.stride_c * (p.out == kElemF32 ? 4 : 2);
+  // Results go through LDS, a block of rows at a time, so that the stores of a
+  // wave cover whole lines: a lane holds four neighbouring columns of one row
+  // in each group of four registers, 32 (MF 16: 16) rows a wave.
+  const rlds_t ep = (rlds_t)lds + T::SUMS + wave * (MF * T::WN * 4 + MF * 4);
+  const rlds_t ep_scale = ep + MF * T::WN * 4;
+  typedef __attribute__((address_space(3))) ri4* lds4_t;
+  typedef __attribute__((address_space(3))) float* lds1_t;
+  const int osz = p.out == kElemF32 ? 4 : 2;
+  char* const c_tile = p.C + (FORM == kFormTN ? group * p.stride_c * osz : 0) + row_c * p.ldc * osz;
+  // Sums up to 2^31 are exact; the conversion to 32-bit floats rounds those
+  // past 2^24 once, to half a unit in the last place.
+  auto value = [&](int bits, float s, float sbc, float bias) {
+    if constexpr (ELEM == kElemI8) return static_cast<float>(bits) * (s * sbc) + bias;
+    else return __builtin_bit_cast(float, bits);
+  };
+  const bool four = n4 + 4 <= p.N;
+  constexpr int EACH = 64 / PIECES, ITER = MF / EACH;  // rows of a store, stores of a block
+  const int c_row = static_cast<int>(p.ldc) * osz;
 #pragma unroll
   for (int i = 0; i < T::FM; ++i) {
-    const int m = am + i * MF + lane % MF;
-    if (m >= rows) continue;
-    const float sa = ELEM == kElemI8 ? p.scale_a[row_c + m] : 0.0f;
+    const int m0 = block_row(i);
+    if (m0 >= rows) break;
+    {
+      const int row = lane % MF;
 #pragma unroll
-    for (int j = 0; j < T::FN; ++j)
+      for (int j = 0; j < T::FN; ++j)
 #pragma unroll
-      for (int r = 0; r < REGS; r += 4) {
-        const int n = n0 + bn + j * MF + (MF == 32 ? 2 * r : 0) + 4 * (lane / MF);
-        const decltype(__builtin_shufflevector(acc[i][j], acc[i][j], 0, 1, 2, 3)) v = {
-            acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]};
-        ragged_store<ELEM>(q, row_c + m, group, n, v, sa);
+        for (int r = 0; r < REGS; r += 4) {
+          const int piece = (j * MF + (MF == 32 ? 2 * r : 0)) / 4 + lane / MF;
+          const decltype(__builtin_shufflevector(acc[i][j], acc[i][j], 0, 1, 2, 3)) v = {
+              acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]};
+          *(lds4_t)(ep + row * (T::WN * 4) + ((piece ^ (row & (PIECES - 1))) * 16)) =
+              __builtin_bit_cast(ri4, v);
+        }
+      if constexpr (ELEM == kElemI8)
+        if (lane < MF) *(lds1_t)(ep_scale + lane * 4) = scale_m[i];
+    }
+    __builtin_amdgcn_wave_barrier();
+    ri4 w[ITER];
+    float s[ITER];
+    int off[ITER];  // of the lane's four results past the tile's start, masked where they are not whole
+    const int row0 = m0 + lane / PIECES;
+    auto take = [&](int it, ri4& v, float& scale) {
+      const int row = it * EACH + lane / PIECES;
+      v = *(lds4_t)(ep + row * (T::WN * 4) + ((c4 ^ (row & (PIECES - 1))) * 16));
+      scale = ELEM == kElemI8 ? *(lds1_t)(ep_scale + row * 4) : 0.0f;
+    };
+#pragma unroll
+    for (int it = 0; it < ITER; ++it) {
+      take(it, w[it], s[it]);
+      off[it] = four && row0 + it * EACH < rows ? (row0 + it * EACH) * c_row + n4 * osz : kRaggedMasked;
+    }
+    // Whole fours by masked buffer stores, which may start at any element.
+    // Without branches, and with the reads of old values apart, no store waits
+    // for the one before it (a 256 x 256 tile of floats: 15.5 thousand cycles
+    // with branches, 9.4 so).
+    auto emit = [&](auto zero) {
+      using O = decltype(zero);
+      typedef O Quad __attribute__((ext_vector_type(4)));
+      const auto to = ragged_rsrc(c_tile, kRaggedMasked);
+      auto store = [&](int it, const float (&v)[4]) {
+        Quad q;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q[e] = static_cast<O>(v[e]);
+        if constexpr (sizeof(O) == 4)
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(ru4, q), to, off[it], 0, 0);
+        else
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(ru2, q), to, off[it], 0, 0);
+      };
+      if (ELEM != kElemI8 && p.beta != 0.0f) {
+        Quad old[ITER];
+#pragma unroll
+        for (int it = 0; it < ITER; ++it)
+          if constexpr (sizeof(O) == 4)
+            old[it] = __builtin_bit_cast(Quad, __builtin_amdgcn_raw_buffer_load_b128(to, off[it], 0, 0));
+          else
+            old[it] = __builtin_bit_cast(Quad, __builtin_amdgcn_raw_buffer_load_b64(to, off[it], 0, 0));
+#pragma unroll
+        for (int it = 0; it < ITER; ++it) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[e] = p.alpha * value(w[it][e], s[it], sb4[e], bias4[e]) + p.beta * static_cast<float>(old[it][e]);
+          store(it, v);
+        }
+      } else {
+#pragma unroll
+        for (int it = 0; it < ITER; ++it) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = value(w[it][e], s[it], sb4[e], bias4[e]);
+            if constexpr (ELEM != kElemI8) v[e] *= p.alpha;
+          }
+          store(it, v);
+        }
       }
+      // The one to three results in front of C's last column.
+      if (!four && n4 < p.N)
+        for (int it = 0; it < ITER && row0 + it * EACH < rows; ++it) {
+          ri4 v;
+          float scale;
+          take(it, v, scale);
+          O* const d = reinterpret_cast<O*>(c_tile + static_cast<long long>(row0 + it * EACH) * c_row) + n4;
+#pragma unroll
+          for (int e = 0; e < 3; ++e)
+            if (n4 + e < p.N) {
+              float x = value(v[e], scale, sb4[e], bias4[e]);
+              if constexpr (ELEM != kElemI8) {
+                x *= p.alpha;
+                if (p.beta != 0.0f) x += p.beta * static_cast<float>(d[e]);
+              }
+              d[e] = static_cast<O>(x);
+            }
+        }
+    };
+    if (p.out == kElemF32) emit(float{});
+    else if (p.out == kElemBF16) emit(__bf16{});
+    else emit(_Float16{});
+    __builtin_amdgcn_wave_barrier();
   }
 #endif
 }
@@ -637,22 +879,49 @@ hipError_t launch_ragged(const RaggedArgs& a, long long grid, hipStream_t stream
   return hipGetLastError();
 }
 
-// The compiled tiles, widest first.
-using RaggedWide = RaggedTile<256, 256, 2, 4, 1, 2, 32, true>;
-using RaggedMid = RaggedTile<128, 128, 2, 2, 1, 2, 32, true>;
-using RaggedMidAny = RaggedTile<128, 128, 2, 2, 1, 2, 32, false>;
-using RaggedThin = RaggedTile<16, 64, 1, 1, 4, 3, 16, true>;
-using RaggedThinAny = RaggedTile<16, 64, 1, 1, 4, 2, 16, false>;
+// The compiled tiles, by the names of RaggedShape.
+//   kWide   eight waves and one workgroup a compute unit.  Weights or operands
+//           whose rows are steps come in rows 4 KiB and more apart: shorter
+//           slices, a deeper ring (bf16 16384 x 2048 x 4096 over 16: 310 us
+//           with 2 slices of 128 bytes, 290 with 3 of 64; transposed weights
+//           272 and 288).
+//   kMid    two workgroups a compute unit.
+//   kDeep   kMid with a ring of four for one workgroup a compute unit, where
+//           there are not tiles for two (2048 x 2048 x 8192: 70 us and 86).
+//   kSmall  three workgroups a compute unit.
+//   kThin, kSlim: few rows, a slice a wave, so that nobody waits for others.
+template <int FORM>
+using RaggedWide = std::conditional_t<FORM == kFormNT, RaggedTile<256, 256, 2, 4, 1, 2, 128, 32, 2>,
+                                      RaggedTile<256, 256, 2, 4, 1, 3, 64, 32, 2>>;
+using RaggedMid = RaggedTile<128, 128, 2, 4, 1, 2, 128, 32, 2>;
+using RaggedDeep = RaggedTile<128, 128, 2, 4, 1, 4, 128, 32, 2>;
+using RaggedSmall = RaggedTile<64, 64, 2, 2, 1, 3, 128, 32, 3>;
+using RaggedThin = RaggedTile<16, 32, 1, 1, 4, 2, 128, 16, 3>;
+using RaggedSlim = RaggedTile<16, 16, 1, 1, 4, 4, 128, 16, 2>;
 
-enum RaggedShape { kWide, kMid, kThin };
+enum RaggedShape { kWide, kMid, kDeep, kSmall, kThin, kSlim, kShapes };
+constexpr int kRaggedRows[kShapes] = {256, 128, 128, 64, 16, 16};  // of a tile
+constexpr int kRaggedCols[kShapes] = {256, 128, 128, 64, 32, 16};
+
+template <int ELEM, int FORM>
+hipError_t launch_shape(int shape, const RaggedArgs& a, long long grid, hipStream_t s) {
+  if constexpr (FORM != kFormTN) {
+    if (shape == kThin) return launch_ragged<ELEM, FORM, RaggedThin>(a, grid, s);
+    if (shape == kSlim) return launch_ragged<ELEM, FORM, RaggedSlim>(a, grid, s);
+  }
+  return shape == kWide   ? launch_ragged<ELEM, FORM, RaggedWide<FORM>>(a, grid, s)
+         : shape == kMid  ? launch_ragged<ELEM, FORM, RaggedMid>(a, grid, s)
+         : shape == kDeep ? launch_ragged<ELEM, FORM, RaggedDeep>(a, grid, s)
+                          : launch_ragged<ELEM, FORM, RaggedSmall>(a, grid, s);
+}
 
 // Largest 2-byte or smaller element count a tile's rows may be apart: the byte
 // offsets of 256 rows fit the 31 bits of a buffer offset.
 constexpr long long kRaggedMaxLd = 1LL << 21;
 
-hipError_t ragged_f32(int form, int shape, bool direct, const RaggedArgs&, long long grid, hipStream_t);
-hipError_t ragged_bf16(int form, int shape, bool direct, const RaggedArgs&, long long grid, hipStream_t);
-hipError_t ragged_f16(int form, int shape, bool direct, const RaggedArgs&, long long grid, hipStream_t);
-hipError_t ragged_i8(int form, int shape, bool direct, const RaggedArgs&, long long grid, hipStream_t);
+hipError_t ragged_f32(int form, int shape, const RaggedArgs&, long long grid, hipStream_t);
+hipError_t ragged_bf16(int form, int shape, const RaggedArgs&, long long grid, hipStream_t);
+hipError_t ragged_f16(int form, int shape, const RaggedArgs&, long long grid, hipStream_t);
+hipError_t ragged_i8(int form, int shape, const RaggedArgs&, long long grid, hipStream_t);
 
 }  // namespace fp32gemm

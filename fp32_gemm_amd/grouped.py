@@ -24,7 +24,7 @@ _SIGS = {
     "quantize_rows": ([_i32, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp], ctypes.c_int),
     "igemm": ([_i32, _i32, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64,
                _vp], ctypes.c_int),
-    "gemm_grouped_plan": ([_i32, _i32, _i32, _i64, _i64, _i64, _i32, ctypes.POINTER(_i32)], _i64),
+    "gemm_grouped_plan": ([_i32, _i32, _i32, _i32, _i64, _i64, _i64, ctypes.POINTER(_i32)], _i64),
     "gemm_grouped_status_string": ([ctypes.c_int], ctypes.c_char_p),
 }
 for _name, (_args, _res) in _SIGS.items():
@@ -51,15 +51,16 @@ def exported_symbols():
     return sorted(_SIGS)
 
 
-def plan(form: str, dtype, groups: int, M: int, N: int, K: int, aligned: bool = True) -> dict:
+def plan(form: str, dtype, groups: int, M: int, N: int, K: int, out=None) -> dict:
     """The tile and workgroups of a product; form "nt", "nn" or "tn" as the
-    kernels see it (transposed weights, plain weights, weight gradient)."""
-    tile = (_i32 * 3)()
-    grid = _lib.gemm_grouped_plan(_FORMS[form], {**_TYPES, **_INT8}[dtype], groups, M, N, K,
-                                  int(aligned), tile)
+    kernels see it (transposed weights, plain weights, weight gradient); out is
+    the output's type (default: the operands', bfloat16 for int8)."""
+    tile = (_i32 * 2)()
+    out = out or (torch.bfloat16 if dtype is torch.int8 else dtype)
+    grid = _lib.gemm_grouped_plan(_FORMS[form], {**_TYPES, **_INT8}[dtype], _TYPES[out], groups, M, N, K, tile)
     if grid < 0:
         raise ValueError("bad arguments")
-    return {"BM": tile[0], "BN": tile[1], "aligned": bool(tile[2]), "grid": grid}
+    return {"BM": tile[0], "BN": tile[1], "grid": grid}
 
 
 def _matrix(t, name, types, dev):

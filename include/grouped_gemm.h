@@ -16,9 +16,8 @@
  * Matrices are row-major with leading dimensions in elements, as in
  * fp32_gemm.h; strides between the groups' weights are in elements too.  All
  * pointers are DEVICE pointers owned by the caller.  Inputs are only read, and
- * only the outputs' windows are written.  Loads of 8- and 16-bit operands that
- * are not aligned to 4 bytes take whole aligned dwords, so up to 3 bytes on
- * either side of such an operand are read (never used).  The library allocates
+ * only the outputs' windows are written; bytes between an operand's rows may be
+ * read (never used), none before its first or past its last.  The library allocates
  * nothing, uses no workspace and keeps no pointer.  Outputs must not overlap
  * inputs.
  *
@@ -26,9 +25,9 @@
  * `stream` (a hipStream_t; NULL = default stream) and nothing else; it may be
  * captured.  Results do not depend on the run: sums are made in a fixed order.
  *
- * Alignment.  Operands whose pointers, leading dimensions and group strides
- * are multiples of 16 bytes, and whose rows are whole 16-byte pieces, take the
- * fastest kernels; anything else is loaded by dwords and shifted into place.
+ * Alignment.  Pointers, leading dimensions and group strides need no more than
+ * their element's alignment.  Rows that start at multiples of 128 bytes and hold
+ * whole slices of 128 bytes (64 halves, 128 integers) are the fastest.
  *
  * Errors: as fp32_gemm.h: validation happens before anything is enqueued; a
  * status -i names the i-th argument, positive ones are SGEMM_ERR_*.
@@ -101,14 +100,13 @@ int igemm(int32_t out_type, int32_t groups, const int32_t* offsets, int64_t M, i
           int64_t stride_b, const float* scale_b, const float* bias, void* C, int64_t ldc,
           void* stream);
 
-/* Which kernel a product would run, without a device.  form: 0 gemm_grouped
+/* The tile a product would run with, without a device.  form: 0 gemm_grouped
  * and igemm with transposed weights, 1 gemm_grouped with K x N weights, 2
- * gemm_grouped_wgrad; type: GEMM_*, or 3 for igemm.  Fills tile[0..1] with the
- * output tile's rows and columns, tile[2] with 1 for the aligned kernel.
- * `aligned` says whether the operands meet the alignment above.  Returns the
- * number of workgroups, or -1 for arguments out of range. */
-int64_t gemm_grouped_plan(int32_t form, int32_t type, int32_t groups, int64_t M, int64_t N,
-                          int64_t K, int32_t aligned, int32_t tile[3]);
+ * gemm_grouped_wgrad; type: GEMM_*, or 3 for igemm; out_type: GEMM_*.  Fills
+ * tile[0..1] with the output tile's rows and columns and returns the number of
+ * workgroups, or -1 for arguments out of range. */
+int64_t gemm_grouped_plan(int32_t form, int32_t type, int32_t out_type, int32_t groups, int64_t M,
+                          int64_t N, int64_t K, int32_t tile[2]);
 
 /* Static string for a status of these calls (never NULL). */
 const char* gemm_grouped_status_string(int status);

@@ -284,9 +284,9 @@ def test_wgrad_rounding_and_accumulation(dtype):
 
 def test_wgrad_wide_tiles():
     g = gen(13)
-    sizes = [300, 20, 0, 129]
+    sizes = [1300, 820, 0, 729]
     off, M = layout(sizes)
-    K, N = 2048 + 8, 2048 + 16
+    K, N = 2048 - 8, 2048 - 16
     assert fg.grouped.plan("tn", BF16, 4, M, N, K)["BM"] == 256
     for dtype in (F32, BF16, F16):
         x, dy = whole(g, (M, K), dtype), whole(g, (M, N), dtype)
@@ -552,3 +552,121 @@ def test_stack_past_two_gigabytes():
     y.fill_(1)
     fg.gemm_grouped_wgrad(x, y, None, dw)
     assert (dw[-1] == 2).all() and not dw[:-1].any()
+
+
+# ---- every tile, at sizes that leave it partly filled -----------------------------
+# tests/test_grouped_host.py checks that these sizes reach every compiled tile.
+
+TILES = [  # rows of the groups, K, N
+    ([700, 513, 0, 1100, 64, 65, 300, 1], 200, 4100),
+    ([700, 400, 0, 300], 500, 2050),
+    ([700, 400, 0, 300], 500, 4100),
+    ([70, 0, 30, 129, 200], 333, 1003),
+    ([17, 1, 0, 5, 9, 20], 520, 1601),
+    ([3], 4000, 1000),
+]
+WGRAD_TILES = [  # type, rows of the groups, K, N
+    (BF16, [700, 0, 333, 1000], 1800, 2040), (BF16, [700, 0, 333, 1000], 500, 300),
+    (BF16, [100, 0, 1, 333, 64, 65, 200, 90], 900, 700), (F32, [33, 0, 70, 5], 777, 301),
+    (BF16, [500, 0, 333, 100], 1000, 1002), (F32, [100, 0, 333, 64, 100, 100], 1001, 1045), (F32, [100, 0, 33, 64], 2000, 2044),
+]
+IGEMM_TILES = [(4090, 4090, 1500), (2100, 3050, 300), (1000, 1700, 900), (130, 1700, 900), (100, 1000, 2000),
+               (1, 4000, 4001), (2040, 2040, 700)]  # M, N, K
+MANY = [((0, 1, 2, 3), 520, 264), ((0, 1, 2, 3), 72, 64), ((600, 257, 0, 512, 400), 72, 520),
+        ((1600, 1257, 0, 1512, 1400), 72, 264)]  # rows of 150 groups in turn, K, N
+
+
+@pytest.mark.parametrize("sizes,K,N", TILES)
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_every_tile(sizes, K, N, trans, dtype):
+    g = gen(70)
+    off, M = layout(sizes, before=1, after=2)
+    E = len(sizes)
+    x = whole(g, (M, K), dtype)
+    w = whole(g, (E, N, K) if trans else (E, K, N), dtype)
+    y = torch.full((M, N), CANARY, device="cuda").to(dtype)
+    fg.gemm_grouped(x, w, offsets_of(off), y, transpose_w=trans)
+    want, _ = grouped_exact(x, w, off, trans)
+    assert torch.equal(y[off[0]:off[-1]], want[off[0]:off[-1]].to(dtype))
+    canary = y.new_tensor(CANARY).float()
+    assert (y[:1].float() == canary).all() and (y[off[-1]:].float() == canary).all()
+
+
+@pytest.mark.parametrize("dtype,sizes,K,N", WGRAD_TILES)
+def test_every_weight_gradient_tile(dtype, sizes, K, N):
+    g = gen(71)
+    off, M = layout(sizes, before=1, after=2)
+    x, dy = whole(g, (M, K), dtype), whole(g, (M, N), dtype)
+    dw = torch.full((len(sizes), K, N), float("nan"), device="cuda", dtype=dtype)
+    fg.gemm_grouped_wgrad(x, dy, offsets_of(off), dw)
+    assert torch.equal(dw, wgrad_exact(x, dy, off)[0].to(dtype))
+
+
+@pytest.mark.parametrize("M,N,K", IGEMM_TILES)
+def test_every_igemm_tile(M, N, K):
+    g = gen(72)
+    a = torch.randint(-128, 128, (M, K), device="cuda", generator=g).to(torch.int8)
+    b = torch.randint(-128, 128, (N, K), device="cuda", generator=g).to(torch.int8)
+    sa = torch.exp2(torch.randint(-8, 0, (M,), device="cuda", generator=g).float())
+    sb = torch.exp2(torch.randint(-8, 0, (N,), device="cuda", generator=g).float())
+    y = torch.full((M, N), float("nan"), device="cuda")
+    fg.igemm(a, sa, b, sb, y)
+    assert torch.equal(y, igemm_exact(a, sa, b, sb, None, [0, M]).float())
+
+
+@pytest.mark.parametrize("each,K,N", MANY)
+def test_more_groups_than_lanes(each, K, N):
+    # Groups past the 64 that a wave looks at together.
+    g = gen(73)
+    sizes = [each[(5 * e + e // 7) % len(each)] for e in range(150)]
+    off, M = layout(sizes, before=2, after=1)
+    x, w = whole(g, (M, K), BF16), whole(g, (150, K, N), BF16)
+    y = torch.full((M, N), CANARY, device="cuda", dtype=F32)
+    fg.gemm_grouped(x, w, offsets_of(off), y)
+    owned = slice(off[0], off[-1])
+    assert torch.equal(y[owned], grouped_exact(x, w, off, False)[0][owned].float())
+    assert (y[:2] == CANARY).all() and (y[off[-1]:] == CANARY).all()
+    dy = whole(g, (M, N), BF16)
+    dw = torch.full((150, K, N), float("nan"), device="cuda")
+    fg.gemm_grouped_wgrad(x, dy, offsets_of(off), dw)
+    assert torch.equal(dw, wgrad_exact(x, dy, off)[0].float())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("K,N", [(1, 3), (3, 1), (2, 2), (7, 7), (200, 3), (5, 130), (1, 1)])
+def test_rows_shorter_than_a_load(dtype, K, N):
+    # Rows of fewer than 16 bytes, over many slices, in every form; the operands
+    # end with their storage.
+    g = gen(74)
+    sizes = [300, 0, 1, 77]
+    off, M = layout(sizes)
+    for trans in (False, True):
+        x, w = whole(g, (M, K), dtype), whole(g, (4, N, K) if trans else (4, K, N), dtype)
+        y = torch.empty(M, N, device="cuda", dtype=dtype)
+        fg.gemm_grouped(x, w, offsets_of(off), y, transpose_w=trans)
+        assert torch.equal(y, grouped_exact(x, w, off, trans)[0].to(dtype))
+        if not trans:
+            tall = whole(g, (1, 1000, N), dtype)
+            xs = whole(g, (40, 1000), dtype, 1)
+            ys = torch.empty(40, N, device="cuda", dtype=F32)
+            fg.gemm_grouped(xs, tall[0], None, ys)
+            assert torch.equal(ys, (xs.double() @ tall[0].double()).float())
+    dy = whole(g, (M, N), dtype)
+    dw = torch.empty(4, K, N, device="cuda", dtype=F32)
+    fg.gemm_grouped_wgrad(x, dy, offsets_of(off), dw)
+    assert torch.equal(dw, wgrad_exact(x, dy, off)[0].float())
+
+
+def test_alpha_beta_on_every_kind_of_tile():
+    g = gen(75)
+    for sizes, K, N in (([700, 600, 900, 512], 64, 2050), ([300, 260], 64, 514), ([70, 65], 64, 67), ([3, 1], 64, 31)):
+        off, M = layout(sizes)
+        x, w, y0 = whole(g, (M, K), BF16), whole(g, (len(sizes), K, N), BF16), whole(g, (M, N), BF16, 50)
+        y = y0.clone()
+        fg.gemm_grouped(x, w, offsets_of(off), y, alpha=0.5, beta=-2.0)
+        assert torch.equal(y, (0.5 * grouped_exact(x, w, off, False)[0] - 2.0 * y0.double()).to(BF16))
+        dy, dw0 = whole(g, (M, N), BF16), whole(g, w.shape, F32, 50)
+        dw = dw0.clone()
+        fg.gemm_grouped_wgrad(x, dy, offsets_of(off), dw, beta=1.0)
+        assert torch.equal(dw, (wgrad_exact(x, dy, off)[0] + dw0.double()).float())

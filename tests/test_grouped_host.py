@@ -115,11 +115,10 @@ def test_status_strings():
 
 @pytest.mark.parametrize("form,dtype", [("nt", torch.int8), ("nt", torch.bfloat16), ("nn", torch.float32),
                                         ("tn", torch.float16)])
-@pytest.mark.parametrize("aligned", [True, False])
-def test_plan_covers_any_split_of_the_rows(form, dtype, aligned):
+def test_plan_covers_any_split_of_the_rows(form, dtype):
     # The grid is sized without the offsets: it must hold the tiles of the worst split.
     for groups, M, N, K in [(1, 1, 64, 64), (64, 7, 100, 64), (8, 1000, 777, 640), (16, 16384, 2048, 4096), (3, 0, 64, 64)]:
-        p = grouped.plan(form, dtype, groups, M, N, K, aligned)
+        p = grouped.plan(form, dtype, groups, M, N, K)
         up = lambda n, t: -(-n // t)  # noqa: E731
         if form == "tn":
             assert p["grid"] == groups * up(up(K, p["BM"]) * up(N, p["BN"]), 8) * 8
@@ -131,6 +130,25 @@ def test_plan_covers_any_split_of_the_rows(form, dtype, aligned):
             assert sum(up(n, p["BM"]) for n in split) * up(N, p["BN"]) <= p["grid"]
     with pytest.raises(ValueError):
         grouped.plan(form, dtype, 0, 1, 1, 1)
+
+
+def test_the_gpu_tests_reach_every_tile():
+    import test_grouped_gpu as on_gpu
+    bf16, every = torch.bfloat16, {(256, 256), (128, 128), (64, 64), (16, 32), (16, 16)}
+
+    def tile(form, dtype, groups, M, N, K):
+        p = grouped.plan(form, dtype, groups, M, N, K)
+        return p["BM"], p["BN"]
+
+    for form in ("nt", "nn"):
+        seen = {tile(form, bf16, len(s), sum(s) + 3, N, K) for s, K, N in on_gpu.TILES}
+        assert seen == (every if form == "nt" else every - {(16, 16)})
+    assert {tile("nt", torch.int8, 1, M, N, K) for M, N, K in on_gpu.IGEMM_TILES} == every
+    for dtype in (bf16, torch.float32):
+        seen = {tile("tn", d, len(s), sum(s) + 3, N, K) for d, s, K, N in on_gpu.WGRAD_TILES if d is dtype}
+        assert seen == {(256, 256), (128, 128), (64, 64)}
+    seen = {tile("nn", bf16, 150, 150 * sum(each) // len(each), N, K) for each, K, N in on_gpu.MANY}
+    assert seen >= {(256, 256), (16, 32)}
 
 
 def test_python_refusals():
