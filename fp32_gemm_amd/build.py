@@ -24,6 +24,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfp32_gemm_amd.so")
+CALLS = os.path.join(PKG, "_torch_calls.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # Packed-FP32 VALU instructions are kept out of every kernel (the
@@ -384,6 +385,7 @@ def build(verbose=True, jobs=None):
             if m and v.get("ScratchSize", 0) > 0:
                 new.add(tuple(int(x) for x in m.groups()[:12]))
         if not new:
+            _build_calls()
             return LIB
         bad = sorted(_spilling() | new)
         with open(SPILLING, "w") as f:
@@ -424,10 +426,33 @@ def _build_once(verbose, jobs):
     return resources
 
 
+def _build_calls():
+    """The module that checks tensors and calls the library for grouped.py:
+    host code against torch's headers, linked to the library beside it."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    tmp = CALLS + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
+    cmd += [f"-I{p}" for p in (*cpp_extension.include_paths(), os.path.join(rocm, "include"),
+                               sysconfig.get_paths()["include"])]
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd += [os.path.join(CSRC, "torch_calls.cpp"), "-o", tmp, f"-L{PKG}", "-lfp32_gemm_amd", f"-L{torch_lib}",
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError("g++ failed on torch_calls.cpp:\n" + p.stderr[-4000:])
+    os.replace(tmp, CALLS)
+
+
 def clean():
     shutil.rmtree(BUILD, ignore_errors=True)
-    if os.path.exists(LIB):
-        os.remove(LIB)
+    for built in (LIB, CALLS):
+        if os.path.exists(built):
+            os.remove(built)
 
 
 if __name__ == "__main__":
