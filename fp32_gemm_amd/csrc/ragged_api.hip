@@ -85,7 +85,7 @@ Plan plan(int form, int type, int out, int groups, long long M, long long N, lon
     }
   }
   // Looking up the order of the lengths takes some 0.4 us of every tile.
-  p.longest_first = form == kFormTN && slices >= 4;
+  p.longest_first = form == kFormTN && slices >= 8;
   p.bm = kRaggedRows[p.shape];
   p.bn = kRaggedCols[p.shape];
   if (form == kFormTN) p.grid = groups * ((tiles(K, p.bm) * tiles(N, p.bn) + 7) / 8 * 8);

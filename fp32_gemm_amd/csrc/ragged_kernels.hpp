@@ -511,12 +511,13 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
     row_c = m0;
   } else {
     TileAt at;
-    if constexpr (T::FM == 4) at = tile_by_fill<T::BM, T::BM / 4, T::BAND>(p, blockIdx.x, tiles_n, lane);
+    if constexpr (T::BM == 256) at = tile_by_fill<T::BM, T::BM / 4, T::BAND>(p, blockIdx.x, tiles_n, lane);
     else at = tile_in_order<T::BM, T::BAND>(p, blockIdx.x, tiles_n, lane);
     group = at.group;
-    if (group < 0) return;
     n0 = at.n * T::BN;
     rows = min(T::BM, at.hi - at.row);
+    // Offsets out of order may count more tiles than an int holds.
+    if (group < 0 || group >= p.groups || at.row < 0 || rows <= 0) return;
     len = p.K;
     a = p.A + at.row * p.lda;
     b = p.B + group * p.stride_b + (B_ALONG ? n0 * p.ldb : static_cast<long long>(n0) * ES);
@@ -655,13 +656,15 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
   };
 
   // A slice through registers: `left` steps of the reduction from step `done`.
-  auto place = [&](int done, int left) {
-    typename LoadA::Held ha;
-    typename LoadB::Held hb;
+  typename LoadA::Held ha;
+  typename LoadB::Held hb;
+  auto fetch = [&](int done, int left) {
     if constexpr (A_ALONG) la.fetch(ha, a + done * ES, done * ES, left * ES, narrow_a, lane);
     else la.fetch(ha, a + done * p.lda, m_bytes, left, narrow_a, lane);
     if constexpr (B_ALONG) lb.fetch(hb, b + done * ES, done * ES, left * ES, narrow_b, lane);
     else lb.fetch(hb, b + done * p.ldb, n0 * ES, left, narrow_b, lane);
+  };
+  auto put = [&] {
     la.put(ha, ring, lane);
     lb.put(hb, ring + T::BM * SL, lane);
   };
@@ -671,7 +674,8 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
   auto run_narrow = [&] {
     for (int t = 0; t < turns; ++t) {
       const int done = (t * T::WAVES_K + kgroup) * STEPS;
-      place(done, min(STEPS, len - done));
+      fetch(done, min(STEPS, len - done));
+      put();
       __syncthreads();
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
@@ -693,6 +697,7 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
     // The first S slices are sent ahead (the last one's B in the first group).
     const bool headed = head > 0 && kgroup == 0;
     if (headed) {
+      fetch(len - head, head);  // first, for its loads to come back first
       la.base += la.step;
       lb.base += lb.step;
       left_a -= T::WAVES_K;
@@ -706,9 +711,9 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
       send_a(s);
       if (s < S - 1) send_b(s);
     }
-    if (headed) place(len - head, head);
-    if constexpr (FORM != kFormTN && T::FM == 4) {
-      const int used = (rows - wave_m * MF + MSTEP - 1) / MSTEP;
+    if (headed) put();
+    if constexpr (FORM != kFormTN && T::BM == 256) {
+      const int used = (rows + 63) / 64;  // quarters of the tile's rows that hold any
       if (used > 3) run(std::integral_constant<int, 4>{});
       else if (used == 3) run(std::integral_constant<int, 3>{});
       else if (used == 2) run(std::integral_constant<int, 2>{});
@@ -900,8 +905,8 @@ using RaggedThin = RaggedTile<16, 32, 1, 1, 4, 2, 128, 16, 3>;
 using RaggedSlim = RaggedTile<16, 16, 1, 1, 4, 4, 128, 16, 2>;
 
 enum RaggedShape { kWide, kMid, kDeep, kSmall, kThin, kSlim, kShapes };
-constexpr int kRaggedRows[kShapes] = {256, 128, 128, 64, 16, 16};  // of a tile
-constexpr int kRaggedCols[kShapes] = {256, 128, 128, 64, 32, 16};
+constexpr int kRaggedRows[kShapes] = {256, 128, 128, 64, RaggedThin::BM, 16};  // of a tile
+constexpr int kRaggedCols[kShapes] = {256, 128, 128, 64, RaggedThin::BN, 16};
 
 template <int ELEM, int FORM>
 hipError_t launch_shape(int shape, const RaggedArgs& a, long long grid, hipStream_t s) {
