@@ -43,10 +43,10 @@ struct Plan {
 // tile's start and end with results of 2 and of 4 bytes.  32-bit floats take
 // four times the matrix instructions a slice.
 struct TileCost { double busy, alone, ends2, ends4; };
-constexpr TileCost kCost16[kShapes] = {{1.4, 1.4, 8, 10},   {.50, .64, 2.3, 3}, {.54, .52, 2.3, 3},
-                                       {.19, .28, 1.0, 1.1}, {.135, .2, .5, .5}, {.09, .11, .5, .5}};
-constexpr TileCost kCost32[kShapes] = {{7.1, 7.1, 10, 10},  {1.9, 1.93, 3, 3},   {1.95, 1.93, 3, 3},
-                                       {.53, .62, 1.1, 1.1}, {.14, .22, .5, .5}, {.09, .11, .5, .5}};
+constexpr TileCost kCost16[kShapes] = {{1.4, 1.4, 7.2, 8.5}, {.50, .64, 2.0, 2.5}, {.54, .52, 2.3, 3},
+                                       {.19, .28, .9, .9},    {.135, .2, .5, .5},   {.09, .11, .5, .5}};
+constexpr TileCost kCost32[kShapes] = {{7.1, 7.1, 8.5, 8.5}, {1.9, 1.93, 2.5, 2.5}, {1.95, 1.93, 3, 3},
+                                       {.52, .62, .8, .8},   {.14, .22, .5, .5},    {.09, .11, .5, .5}};
 
 // The shape whose tiles, spread over the compute units, are done first by these
 // costs.  The offsets are on the device, so groups are taken as equal but for

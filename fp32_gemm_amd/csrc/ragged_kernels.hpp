@@ -893,14 +893,20 @@ hipError_t launch_ragged(const RaggedArgs& a, long long grid, hipStream_t stream
 //   kMid    two workgroups a compute unit.
 //   kDeep   kMid with a ring of four for one workgroup a compute unit, where
 //           there are not tiles for two (2048 x 2048 x 8192: 70 us and 86).
-//   kSmall  three workgroups a compute unit.
+//   kSmall  three workgroups a compute unit; five, with rings of two, for
+//           weight gradients, whose reductions are often short (bf16, 32
+//           experts of 16 rows, 1024 x 1024: 35 us and 43 with rings of three;
+//           bf16 products 1024 x 1024 x 8192 65 and 38, f32 4097 x 1024 x 2048
+//           over 8 experts 187 and 159).
 //   kThin, kSlim: few rows, a slice a wave, so that nobody waits for others.
 template <int FORM>
 using RaggedWide = std::conditional_t<FORM == kFormNT, RaggedTile<256, 256, 2, 4, 1, 2, 128, 32, 2>,
                                       RaggedTile<256, 256, 2, 4, 1, 3, 64, 32, 2>>;
 using RaggedMid = RaggedTile<128, 128, 2, 4, 1, 2, 128, 32, 2>;
 using RaggedDeep = RaggedTile<128, 128, 2, 4, 1, 4, 128, 32, 2>;
-using RaggedSmall = RaggedTile<64, 64, 2, 2, 1, 3, 128, 32, 3>;
+template <int FORM>
+using RaggedSmall = std::conditional_t<FORM == kFormTN, RaggedTile<64, 64, 2, 2, 1, 2, 128, 32, 4>,
+                                       RaggedTile<64, 64, 2, 2, 1, 3, 128, 32, 3>>;
 using RaggedThin = RaggedTile<16, 32, 1, 1, 4, 2, 128, 16, 3>;
 using RaggedSlim = RaggedTile<16, 16, 1, 1, 4, 4, 128, 16, 2>;
 
@@ -917,7 +923,7 @@ hipError_t launch_shape(int shape, const RaggedArgs& a, long long grid, hipStrea
   return shape == kWide   ? launch_ragged<ELEM, FORM, RaggedWide<FORM>>(a, grid, s)
          : shape == kMid  ? launch_ragged<ELEM, FORM, RaggedMid>(a, grid, s)
          : shape == kDeep ? launch_ragged<ELEM, FORM, RaggedDeep>(a, grid, s)
-                          : launch_ragged<ELEM, FORM, RaggedSmall>(a, grid, s);
+                          : launch_ragged<ELEM, FORM, RaggedSmall<FORM>>(a, grid, s);
 }
 
 // Largest 2-byte or smaller element count a tile's rows may be apart: the byte

@@ -569,11 +569,12 @@ WGRAD_TILES = [  # type, rows of the groups, K, N
     (BF16, [700, 0, 333, 1000], 1800, 2040), (BF16, [700, 0, 333, 1000], 500, 300),
     (BF16, [100, 0, 1, 333, 64, 65, 200, 90], 900, 700), (F32, [33, 0, 70, 5], 777, 301),
     (BF16, [500, 0, 333, 100], 1000, 1002), (F32, [100, 0, 333, 64, 100, 100], 1001, 1045), (F32, [100, 0, 33, 64], 2000, 2044),
+    (F32, [300, 200, 333], 2000, 2044),
 ]
 IGEMM_TILES = [(4090, 4090, 1500), (2100, 3050, 300), (1000, 1700, 900), (130, 1700, 900), (100, 1000, 2000),
                (1, 4000, 4001), (2040, 2040, 700)]  # M, N, K
 MANY = [((0, 1, 2, 3), 520, 264), ((0, 1, 2, 3), 72, 64), ((600, 257, 0, 512, 400), 72, 520),
-        ((1600, 1257, 0, 1512, 1400), 72, 264)]  # rows of 150 groups in turn, K, N
+        ((1600, 1257, 0, 1512, 1400), 520, 512)]  # rows of 150 groups in turn, K, N
 
 
 @pytest.mark.parametrize("sizes,K,N", TILES)
