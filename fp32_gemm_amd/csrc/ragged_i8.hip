@@ -36,46 +36,49 @@ __device__ __forceinline__ int code_of(float x, double inv) {
 // One row by THREADS threads of a 256-thread workgroup.  The largest magnitude
 // is an integer maximum over the bits without the sign, in which infinities
 // and NaN exceed every number: such a row gets the scale NaN and codes 0.
-// VEC: rows are whole, aligned 16-byte pieces of x and aligned groups of q.
-// Up to KEEP pieces a thread stay in registers as they came, longer rows are
-// read twice.  Memory-bound: bf16 8192 x 8192 in 38.6 us,
+// Rows are read in pieces of 16 bytes from any element on, their last few
+// elements one a thread.  Up to KEEP pieces a thread stay in registers as they
+// came, longer rows are read twice.  Memory-bound: bf16 8192 x 8192 in 38.6 us,
 // 5.2 TB/s, as a copy runs (59.6 with every code in 64 bits).
 constexpr int kQuantKeep = 8;
-template <int ELEM, int THREADS, bool VEC>
+template <int ELEM, int THREADS>
 __global__ __launch_bounds__(256) void quantize_kernel(const char* x, long long ldx, signed char* q,
                                                        long long ldq, float* scale, int M, int K) {
-  constexpr int ES = elem_size(ELEM), PER = VEC ? 16 / ES : 1;
+  constexpr int ES = elem_size(ELEM), PER = 16 / ES;
   const int in = threadIdx.x % THREADS;
   const long long row = static_cast<long long>(blockIdx.x) * (256 / THREADS) + threadIdx.x / THREADS;
   const bool live = row < M;
   const char* src = x + (live ? row : 0) * ldx * ES;
   signed char* dst = q + (live ? row : 0) * ldq;
-  const int pieces = live ? K / PER : 0;
+  const int pieces = live ? K / PER : 0, rest = live ? K % PER : 0;
+  const bool one = in < rest;  // this thread takes an element of the rest
 
-  using Raw = std::conditional_t<VEC, ri4, float>;
-  Raw keep[kQuantKeep];
+  ri4 keep[kQuantKeep];
   unsigned top = 0;
-  auto load = [&](int c) -> Raw {
-    if constexpr (VEC) return reinterpret_cast<const ri4*>(src)[c];
-    else return as_float<ELEM>(src, c);
+  auto load = [&](int c) {
+    ri4 w;
+    __builtin_memcpy(&w, src + static_cast<long long>(c) * 16, 16);
+    return w;
   };
-  auto value = [&](const Raw& w, int i) -> float {
-    if constexpr (!VEC) return w;
-    else if constexpr (ELEM == kElemF32) return __builtin_bit_cast(rf4, w)[i];
+  auto value = [&](const ri4& w, int i) -> float {
+    if constexpr (ELEM == kElemF32) return __builtin_bit_cast(rf4, w)[i];
     else if constexpr (ELEM == kElemBF16) return static_cast<float>(__builtin_bit_cast(rb8, w)[i]);
     else return static_cast<float>(__builtin_bit_cast(rh8, w)[i]);
   };
-  auto raise = [&](const Raw& w) {
+  auto lift = [&](float v) { top = max(top, __builtin_bit_cast(unsigned, v) & 0x7FFFFFFFu); };
+  auto raise = [&](const ri4& w) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) top = max(top, __builtin_bit_cast(unsigned, value(w, i)) & 0x7FFFFFFFu);
+    for (int i = 0; i < PER; ++i) lift(value(w, i));
   };
 #pragma unroll
   for (int j = 0; j < kQuantKeep; ++j) {
     const int c = in + j * THREADS;
-    keep[j] = c < pieces ? load(c) : Raw{};
+    keep[j] = c < pieces ? load(c) : ri4{};
   }
+  const float last = one ? as_float<ELEM>(src, static_cast<long long>(pieces) * PER + in) : 0.0f;
 #pragma unroll
   for (int j = 0; j < kQuantKeep; ++j) raise(keep[j]);
+  lift(last);
   for (int c = in + kQuantKeep * THREADS; c < pieces; c += THREADS) raise(load(c));
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) top = max(top, static_cast<unsigned>(__shfl_xor(static_cast<int>(top), d)));
@@ -94,7 +97,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(const char* x, long long 
   const float inv32 = small ? 0.0f : static_cast<float>(inv);
   if (live && in == 0)
     scale[row] = top >= 0x7F800000u ? __builtin_nanf("") : static_cast<float>(static_cast<double>(largest) / 127.0);
-  auto write = [&](int c, const Raw& w) {
+  auto write = [&](int c, const ri4& w) {
     int code[PER];
     bool near = small;
 #pragma unroll
@@ -106,42 +109,35 @@ __global__ __launch_bounds__(256) void quantize_kernel(const char* x, long long 
     if (near)
 #pragma unroll
       for (int i = 0; i < PER; ++i) code[i] = code_of(value(w, i), inv);
-    if (!usable)
+    unsigned o[PER / 4];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) code[i] = 0;
-    if constexpr (VEC) {
-      unsigned o[PER / 4];
-#pragma unroll
-      for (int i = 0; i < PER / 4; ++i)
-        o[i] = (code[4 * i] & 255u) | (code[4 * i + 1] & 255u) << 8 | (code[4 * i + 2] & 255u) << 16 |
-               static_cast<unsigned>(code[4 * i + 3]) << 24;
-      if constexpr (PER == 8) reinterpret_cast<ri2*>(dst)[c] = ri2{static_cast<int>(o[0]), static_cast<int>(o[1])};
-      else reinterpret_cast<unsigned*>(dst)[c] = o[0];
-    } else {
-      dst[c] = static_cast<signed char>(code[0]);
-    }
+    for (int i = 0; i < PER / 4; ++i)
+      o[i] = usable ? (code[4 * i] & 255u) | (code[4 * i + 1] & 255u) << 8 | (code[4 * i + 2] & 255u) << 16 |
+                          static_cast<unsigned>(code[4 * i + 3]) << 24
+                    : 0u;
+    __builtin_memcpy(dst + static_cast<long long>(c) * PER, o, PER);
   };
 #pragma unroll
   for (int j = 0; j < kQuantKeep; ++j) {
     const int c = in + j * THREADS;
     if (c < pieces) write(c, keep[j]);
   }
+  if (one)
+    dst[static_cast<long long>(pieces) * PER + in] = static_cast<signed char>(usable ? code_of(last, inv) : 0);
   for (int c = in + kQuantKeep * THREADS; c < pieces; c += THREADS) write(c, load(c));
 }
 
 template <int ELEM>
 void launch_quantize(const char* x, long long ldx, signed char* q, long long ldq, float* scale, int M,
                      int K, hipStream_t s) {
-  constexpr int ES = elem_size(ELEM), PER = 16 / ES;
-  const bool vec = K % PER == 0 && ldx % PER == 0 && ldq % PER == 0 &&
-                   reinterpret_cast<uintptr_t>(x) % 16 == 0 && reinterpret_cast<uintptr_t>(q) % PER == 0;
-  // A wave takes rows of up to two pieces a lane; longer ones go to four waves.
-  const bool wave = (vec ? K / PER : K) <= 128;
+  // A wave takes rows of up to two pieces a lane, and of up to eight where there
+  // are rows enough for all waves (bf16 8192 x 4097: 20.5 us, 25.1 by four); longer
+  // ones go to four waves.
+  const int pieces = K / (16 / elem_size(ELEM));
+  const bool wave = pieces <= 128 || (pieces <= 64 * kQuantKeep && M >= 4096);
   const dim3 grid(static_cast<unsigned>(wave ? (M + 3) / 4 : M));
-  if (vec && wave) quantize_kernel<ELEM, 64, true><<<grid, 256, 0, s>>>(x, ldx, q, ldq, scale, M, K);
-  else if (vec) quantize_kernel<ELEM, 256, true><<<grid, 256, 0, s>>>(x, ldx, q, ldq, scale, M, K);
-  else if (wave) quantize_kernel<ELEM, 64, false><<<grid, 256, 0, s>>>(x, ldx, q, ldq, scale, M, K);
-  else quantize_kernel<ELEM, 256, false><<<grid, 256, 0, s>>>(x, ldx, q, ldq, scale, M, K);
+  if (wave) quantize_kernel<ELEM, 64><<<grid, 256, 0, s>>>(x, ldx, q, ldq, scale, M, K);
+  else quantize_kernel<ELEM, 256><<<grid, 256, 0, s>>>(x, ldx, q, ldq, scale, M, K);
 }
 
 }  // namespace

@@ -389,6 +389,21 @@ def test_quantize_long_rows_and_strides():
         assert (qb == 55).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("M,K", [(4100, 2049), (4096, 1030), (4097, 129), (300, 5001)])
+def test_quantize_many_rows(dtype, M, K):
+    # 127 x is exact in 64 bits, and the quotient lies on a tie or at least 2^-33
+    # from one, so rounding it once in 64 bits moves nothing across.
+    x = normal(gen(31), (M, K), dtype)
+    x[::7] *= 2.0 ** -13
+    q = torch.full((M, K), 99, dtype=torch.int8, device="cuda")
+    s = torch.full((M,), -1.0, device="cuda")
+    fg.quantize_rows(x, q, s)
+    top = x.double().abs().amax(1)
+    assert torch.equal(q, torch.round(x.double() * 127 / top[:, None]).to(torch.int8))
+    assert ((s.double() - top / 127).abs() <= 2.0 ** -24 * top / 127).all()
+
+
 def igemm_exact(a, sa, b, sb, bias, off):
     """Groups' products in 64 bits (whole numbers up to 2^31 are exact there)."""
     M, N = a.shape[0], b.shape[-2]
