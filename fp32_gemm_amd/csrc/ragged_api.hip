@@ -52,7 +52,7 @@ constexpr TileCost kCost32[kShapes] = {{7.1, 7.1, 8.5, 8.5}, {1.9, 1.93, 2.5, 2.
 // costs.  The offsets are on the device, so groups are taken as equal but for
 // the last row tile of each, which is half full.
 Plan plan(int form, int type, int out, int groups, long long M, long long N, long long K) {
-  constexpr double kUnits = 256;
+  constexpr double kUnits = 256, kLongSlices = 8;
   auto tiles = [](long long n, int t) { return (n + t - 1) / t; };
   const long long used = std::min<long long>(groups, M);
   const TileCost* cost = type == kElemF32 ? kCost32 : kCost16;
@@ -75,7 +75,11 @@ Plan plan(int form, int type, int out, int groups, long long M, long long N, lon
     double n = count / kUnits;
     if (shape == kWide && form != kFormTN && groups > 1) n = n <= 1 ? 1 : n + 0.4;
     else if (shape <= kDeep) n = std::ceil(n);
-    else if (shape == kSmall && n > 1) n += 0.5;
+    // Long reductions of ragged groups: where all tiles are resident at once,
+    // long ones share a unit to the end; one at a time, the longest first, they
+    // even out (f32, 8000 rows over 8, 1024 x 1024: 164 us and 136).
+    if (form == kFormTN && groups > 1 && shape == kMid && n == 2 && slices >= kLongSlices) n = 2.5;
+    if (shape == kSmall && n > 1) n += 0.5;
     const double busy = c.busy * (form == kFormNN && shape == kThin ? 1.5 : 1.0);
     const double time = std::max(n * busy, c.alone) * slices +
                         std::max(n, 1.0) * (out == kElemF32 ? c.ends4 : c.ends2);
@@ -85,7 +89,7 @@ Plan plan(int form, int type, int out, int groups, long long M, long long N, lon
     }
   }
   // Looking up the order of the lengths takes some 0.4 us of every tile.
-  p.longest_first = form == kFormTN && slices >= 8;
+  p.longest_first = form == kFormTN && slices >= kLongSlices;
   p.bm = kRaggedRows[p.shape];
   p.bn = kRaggedCols[p.shape];
   if (form == kFormTN) p.grid = groups * ((tiles(K, p.bm) * tiles(N, p.bn) + 7) / 8 * 8);
