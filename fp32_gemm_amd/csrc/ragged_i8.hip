@@ -128,26 +128,27 @@ __global__ __launch_bounds__(256) void quantize_kernel(const char* x, long long 
 }
 
 template <int ELEM>
-void launch_quantize(const char* x, long long ldx, signed char* q, long long ldq, float* scale, int M,
-                     int K, hipStream_t s) {
+hipError_t launch_quantize(const char* x, long long ldx, signed char* q, long long ldq, float* scale, int M,
+                           int K, hipStream_t s) {
   // A wave takes rows of up to two pieces a lane, and of up to eight where there
   // are rows enough for all waves (bf16 8192 x 4097: 20.5 us, 25.1 by four); longer
   // ones go to four waves.
   const int pieces = K / (16 / elem_size(ELEM));
   const bool wave = pieces <= 128 || (pieces <= 64 * kQuantKeep && M >= 4096);
   const dim3 grid(static_cast<unsigned>(wave ? (M + 3) / 4 : M));
-  if (wave) quantize_kernel<ELEM, 64><<<grid, 256, 0, s>>>(x, ldx, q, ldq, scale, M, K);
-  else quantize_kernel<ELEM, 256><<<grid, 256, 0, s>>>(x, ldx, q, ldq, scale, M, K);
+  void* values[] = {&x, &ldx, &q, &ldq, &scale, &M, &K};
+  return hipLaunchKernel(wave ? reinterpret_cast<const void*>(&quantize_kernel<ELEM, 64>)
+                              : reinterpret_cast<const void*>(&quantize_kernel<ELEM, 256>),
+                         grid, dim3(256), values, 0, s);
 }
 
 }  // namespace
 
 hipError_t quantize_launch(int type, const char* x, long long ldx, signed char* q, long long ldq,
                            float* scale, int M, int K, hipStream_t s) {
-  if (type == kElemF32) launch_quantize<kElemF32>(x, ldx, q, ldq, scale, M, K, s);
-  else if (type == kElemBF16) launch_quantize<kElemBF16>(x, ldx, q, ldq, scale, M, K, s);
-  else launch_quantize<kElemF16>(x, ldx, q, ldq, scale, M, K, s);
-  return hipGetLastError();
+  return type == kElemF32    ? launch_quantize<kElemF32>(x, ldx, q, ldq, scale, M, K, s)
+         : type == kElemBF16 ? launch_quantize<kElemBF16>(x, ldx, q, ldq, scale, M, K, s)
+                             : launch_quantize<kElemF16>(x, ldx, q, ldq, scale, M, K, s);
 }
 
 }  // namespace fp32gemm

@@ -884,10 +884,14 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
 #endif
 }
 
+// Launches return their own error: hipGetLastError() would also give, and
+// clear, one that the program left from an earlier call of its own.
 template <int ELEM, int FORM, class T>
 hipError_t launch_ragged(const RaggedArgs& a, long long grid, hipStream_t stream) {
-  ragged_kernel<ELEM, FORM, T><<<dim3(static_cast<unsigned>(grid)), dim3(T::NT), 0, stream>>>(a);
-  return hipGetLastError();
+  RaggedArgs args = a;
+  void* values[] = {&args};
+  return hipLaunchKernel(reinterpret_cast<const void*>(&ragged_kernel<ELEM, FORM, T>),
+                         dim3(static_cast<unsigned>(grid)), dim3(T::NT), values, 0, stream);
 }
 
 // The compiled tiles, by the names of RaggedShape.
