@@ -61,8 +61,7 @@ Plan plan(int form, int type, int out, int groups, long long M, long long N, lon
   Plan p{};
   double best = 0;
   for (int shape = 0; shape < kShapes; ++shape) {
-    // Where rows of W are steps, few columns are short pieces of many rows.
-    if ((form == kFormTN && shape == kThin) || (form != kFormNT && shape == kSlim)) continue;
+    if (!ragged_compiled(type, form, shape)) continue;
     const int bm = kRaggedRows[shape], bn = kRaggedCols[shape];
     const TileCost& c = cost[shape];
     double count;  // tiles
@@ -121,6 +120,12 @@ int launch(int type, int form, const RaggedArgs& a, long long M, long long N, lo
 
 bool float_type(int t) { return t == GEMM_F32 || t == GEMM_BF16 || t == GEMM_F16; }
 long long at_least(long long n) { return n > 1 ? n : 1; }
+
+bool plan_arguments(int form, int type, int out_type, int groups, long long M, long long N, long long K) {
+  return form >= kFormNT && form <= kFormTN && type >= kElemF32 && type <= kElemI8 &&
+         (type != kElemI8 || form == kFormNT) && float_type(out_type) && groups >= 1 && groups <= kMaxGroups &&
+         M >= 0 && N >= 0 && K >= 0 && M <= kMaxDim && N <= kMaxDim && K <= kMaxDim;
+}
 
 }  // namespace
 }  // namespace fp32gemm
@@ -300,16 +305,25 @@ int igemm(int32_t out_type, int32_t groups, const int32_t* offsets, int64_t M, i
 
 int64_t gemm_grouped_plan(int32_t form, int32_t type, int32_t out_type, int32_t groups, int64_t M,
                           int64_t N, int64_t K, int32_t tile[2]) {
-  if (form < kFormNT || form > kFormTN || type < kElemF32 || type > kElemI8 ||
-      (type == kElemI8 && form != kFormNT) || !float_type(out_type) || groups < 1 ||
-      groups > kMaxGroups || M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim ||
-      tile == nullptr)
-    return -1;
+  if (tile == nullptr || !plan_arguments(form, type, out_type, groups, M, N, K)) return -1;
   const Plan p = plan(form, type, out_type, groups, M, N, K);
   if (p.grid > kMaxGrid) return -1;
   tile[0] = p.bm;
   tile[1] = p.bn;
   return p.grid;
+}
+
+int32_t gemm_grouped_tile(int32_t form, int32_t type, int32_t out_type, int32_t groups, int64_t M,
+                          int64_t N, int64_t K) {
+  if (!plan_arguments(form, type, out_type, groups, M, N, K)) return -1;
+  return plan(form, type, out_type, groups, M, N, K).shape;
+}
+
+int32_t gemm_grouped_tiles(int32_t form, int32_t type) {
+  if (!plan_arguments(form, type, GEMM_F32, 1, 0, 0, 0)) return -1;
+  int32_t bits = 0;
+  for (int shape = 0; shape < kShapes; ++shape) bits |= ragged_compiled(type, form, shape) << shape;
+  return bits;
 }
 
 const char* gemm_grouped_status_string(int status) {

@@ -924,16 +924,39 @@ enum RaggedShape { kWide, kMid, kDeep, kSmall, kThin, kSlim, kShapes };
 constexpr int kRaggedRows[kShapes] = {256, 128, 128, 64, RaggedThin::BM, 16};  // of a tile
 constexpr int kRaggedCols[kShapes] = {256, 128, 128, 64, RaggedThin::BN, 16};
 
+// The shapes that the plan may choose for a type and form, and no others, are
+// compiled.  Where rows of W are steps, few columns are short pieces of many
+// rows, and a weight gradient has no few rows.  32-bit products wait for the
+// matrix cores, not for loads: there kDeep is never the cheaper of the two but
+// for weight gradients.
+constexpr bool ragged_compiled(int elem, int form, int shape) {
+  return shape == kSlim   ? form == kFormNT
+         : shape == kThin ? form != kFormTN
+         : shape == kDeep ? elem != kElemF32 || form == kFormTN
+                          : true;
+}
+
+template <int ELEM, int FORM, int SHAPE, class T>
+bool launch_if(int shape, const RaggedArgs& a, long long grid, hipStream_t s, hipError_t& err) {
+  if constexpr (ragged_compiled(ELEM, FORM, SHAPE)) {
+    if (shape != SHAPE) return false;
+    err = launch_ragged<ELEM, FORM, T>(a, grid, s);
+    return true;
+  } else {
+    return false;
+  }
+}
+
 template <int ELEM, int FORM>
 hipError_t launch_shape(int shape, const RaggedArgs& a, long long grid, hipStream_t s) {
-  if constexpr (FORM != kFormTN) {
-    if (shape == kThin) return launch_ragged<ELEM, FORM, RaggedThin>(a, grid, s);
-    if (shape == kSlim) return launch_ragged<ELEM, FORM, RaggedSlim>(a, grid, s);
-  }
-  return shape == kWide   ? launch_ragged<ELEM, FORM, RaggedWide<FORM>>(a, grid, s)
-         : shape == kMid  ? launch_ragged<ELEM, FORM, RaggedMid>(a, grid, s)
-         : shape == kDeep ? launch_ragged<ELEM, FORM, RaggedDeep>(a, grid, s)
-                          : launch_ragged<ELEM, FORM, RaggedSmall<FORM>>(a, grid, s);
+  hipError_t err = hipErrorInvalidValue;
+  launch_if<ELEM, FORM, kWide, RaggedWide<FORM>>(shape, a, grid, s, err) ||
+      launch_if<ELEM, FORM, kMid, RaggedMid>(shape, a, grid, s, err) ||
+      launch_if<ELEM, FORM, kDeep, RaggedDeep>(shape, a, grid, s, err) ||
+      launch_if<ELEM, FORM, kSmall, RaggedSmall<FORM>>(shape, a, grid, s, err) ||
+      launch_if<ELEM, FORM, kThin, RaggedThin>(shape, a, grid, s, err) ||
+      launch_if<ELEM, FORM, kSlim, RaggedSlim>(shape, a, grid, s, err);
+  return err;
 }
 
 // Largest 2-byte or smaller element count a tile's rows may be apart: the byte

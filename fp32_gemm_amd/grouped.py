@@ -26,6 +26,8 @@ _SIGS = {
     "igemm": ([_i32, _i32, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64,
                _vp], ctypes.c_int),
     "gemm_grouped_plan": ([_i32, _i32, _i32, _i32, _i64, _i64, _i64, ctypes.POINTER(_i32)], _i64),
+    "gemm_grouped_tile": ([_i32, _i32, _i32, _i32, _i64, _i64, _i64], _i32),
+    "gemm_grouped_tiles": ([_i32, _i32], _i32),
     "gemm_grouped_status_string": ([ctypes.c_int], ctypes.c_char_p),
 }
 for _name, (_args, _res) in _SIGS.items():
@@ -52,16 +54,28 @@ def exported_symbols():
     return sorted(_SIGS)
 
 
+TILES = ("256x256", "128x128", "128x128 deep", "64x64", "16x32", "16x16")
+
+
 def plan(form: str, dtype, groups: int, M: int, N: int, K: int, out=None) -> dict:
     """The tile and workgroups of a product; form "nt", "nn" or "tn" as the
     kernels see it (transposed weights, plain weights, weight gradient); out is
     the output's type (default: the operands', bfloat16 for int8)."""
     tile = (_i32 * 2)()
     out = out or (torch.bfloat16 if dtype is torch.int8 else dtype)
-    grid = _lib.gemm_grouped_plan(_FORMS[form], {**_TYPES, **_INT8}[dtype], _TYPES[out], groups, M, N, K, tile)
+    args = (_FORMS[form], {**_TYPES, **_INT8}[dtype], _TYPES[out], groups, M, N, K)
+    grid = _lib.gemm_grouped_plan(*args, tile)
     if grid < 0:
         raise ValueError("bad arguments")
-    return {"BM": tile[0], "BN": tile[1], "grid": grid}
+    return {"BM": tile[0], "BN": tile[1], "grid": grid, "tile": TILES[_lib.gemm_grouped_tile(*args)]}
+
+
+def tiles(form: str, dtype) -> list:
+    """The tiles that a form and type can run with."""
+    bits = _lib.gemm_grouped_tiles(_FORMS[form], {**_TYPES, **_INT8}[dtype])
+    if bits < 0:
+        raise ValueError("bad arguments")
+    return [name for i, name in enumerate(TILES) if bits >> i & 1]
 
 
 def gemm_grouped(X, W, offsets, Y, alpha=1.0, beta=0.0, transpose_w=False, stream=None):

@@ -108,6 +108,15 @@ int igemm(int32_t out_type, int32_t groups, const int32_t* offsets, int64_t M, i
 int64_t gemm_grouped_plan(int32_t form, int32_t type, int32_t out_type, int32_t groups, int64_t M,
                           int64_t N, int64_t K, int32_t tile[2]);
 
+/* The same tile's index: 0 256x256, 1 128x128, 2 128x128 with more slices on
+ * their way, 3 64x64, 4 16x32, 5 16x16; -1 for arguments out of range. */
+int32_t gemm_grouped_tile(int32_t form, int32_t type, int32_t out_type, int32_t groups, int64_t M,
+                          int64_t N, int64_t K);
+
+/* The tiles that a form and type can run with: bit i for index i; -1 for
+ * arguments out of range. */
+int32_t gemm_grouped_tiles(int32_t form, int32_t type);
+
 /* Static string for a status of these calls (never NULL). */
 const char* gemm_grouped_status_string(int status);
 

@@ -45,3 +45,85 @@ def test_an_earlier_error_is_left_to_the_program():
     assert left != 0
     want = torch.cat([x[:10].double() @ w[0].double(), x[10:].double() @ w[1].double()])
     assert torch.equal(y, want.to(BF16))
+
+
+# ---- every compiled tile of every form and type ------------------------------------
+# tests/test_grouped_edges_host.py checks that these sizes reach each of them.
+
+PRODUCTS = [  # rows of the groups, K, N
+    ([10, 6, 0, 1], 349, 77),
+    ([1, 14, 51, 0], 303, 3755),
+    ([250, 0, 258, 262, 209, 116, 174, 1], 307, 2139),
+    ([4, 0, 4, 1], 353, 1713),
+    ([941, 321, 0, 1253, 663, 976, 1, 346], 301, 2881),
+    ([1, 147, 119, 187, 140, 78, 204, 0], 311, 4053),
+    ([67, 45, 1, 101, 49, 84, 0, 81], 661, 4059),
+]
+WEIGHT_GRADIENTS = [  # rows of the groups, K, N
+    ([121, 1, 337, 0], 247, 85),
+    ([1, 0, 200, 91], 203, 3045),
+    ([0, 310, 100, 1, 75], 751, 3543),
+    ([0, 130, 20, 1, 75], 751, 3543),
+    ([1, 0, 77, 31], 203, 3045),
+    ([149, 240, 172, 351, 1, 518, 0, 285], 1555, 133),
+    ([211, 563, 261, 1, 359, 155, 282, 0], 217, 3653),
+]
+
+
+def layout(sizes):
+    """Offsets of groups that leave one row in front and two behind."""
+    off = [1]
+    for n in sizes:
+        off.append(off[-1] + n)
+    return off, off[-1] + 2
+
+
+def spans(off):
+    return [slice(off[e], off[e + 1]) for e in range(len(off) - 1)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("sizes,K,N", PRODUCTS)
+def test_products_in_every_tile(sizes, K, N, transposed, dtype):
+    # Whole numbers: sums are exact in 32 bits, the result is rounded once.
+    g = gen(2)
+    off, M = layout(sizes)
+    x = whole(g, (M, K), dtype)
+    w = whole(g, (len(sizes), N, K) if transposed else (len(sizes), K, N), dtype)
+    y = torch.full((M, N), 77.0, device="cuda", dtype=dtype)
+    want = y.clone()
+    for e, rows in enumerate(spans(off)):
+        we = w[e].double()
+        want[rows] = (x[rows].double() @ (we.t().contiguous() if transposed else we)).to(dtype)
+    fg.gemm_grouped(x, w, offsets_of(off), y, transpose_w=transposed)
+    assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("sizes,K,N", WEIGHT_GRADIENTS)
+def test_weight_gradients_in_every_tile(sizes, K, N, dtype):
+    g = gen(3)
+    off, M = layout(sizes)
+    x, dy = whole(g, (M, K), dtype), whole(g, (M, N), dtype)
+    dw = torch.full((len(sizes), K, N), float("nan"), device="cuda", dtype=dtype)
+    fg.gemm_grouped_wgrad(x, dy, offsets_of(off), dw)
+    want = torch.stack([x[rows].double().t().contiguous() @ dy[rows].double() for rows in spans(off)])
+    assert torch.equal(dw, want.to(dtype))
+
+
+@pytest.mark.parametrize("sizes,K,N", PRODUCTS)
+def test_8_bit_products_in_every_tile(sizes, K, N):
+    g = gen(4)
+    off, M = layout(sizes)
+    E = len(sizes)
+    a, b = whole(g, (M, K), torch.int8, 127), whole(g, (E, N, K), torch.int8, 127)
+    # Powers of two, and sums below 2^24: the result is exact in 32 bits.
+    sa = torch.exp2(torch.randint(-8, 0, (M,), device="cuda", generator=g).float())
+    sb = torch.exp2(torch.randint(-8, 0, (E, N), device="cuda", generator=g).float())
+    y = torch.full((M, N), 77.0, device="cuda")
+    want = y.clone()
+    for e, rows in enumerate(spans(off)):
+        want[rows] = ((a[rows].double() @ b[e].double().t().contiguous()) * sa[rows, None].double() * sb[e].double()).float()
+    fg.igemm(a, sa, b, sb, y, offsets=offsets_of(off))
+    assert torch.equal(y, want)
