@@ -22,3 +22,10 @@ def test_tiles_refuse_what_does_not_exist():
         grouped.tiles("nn", I8)
     assert grouped._lib.gemm_grouped_tile(0, 4, 0, 1, 1, 1, 1) == -1
     assert grouped._lib.gemm_grouped_tile(0, 0, 0, 0, 1, 1, 1) == -1
+
+
+def test_long_weight_gradients_of_two_tiles_a_unit():
+    # 512 tiles of 128 x 128: in 32 bits one resident tile a unit is faster where
+    # groups differ in length, in 16 bits two are, or are as fast.
+    for dtype, tile in ((F32, "128x128 deep"), (BF16, "128x128"), (F16, "128x128")):
+        assert grouped.plan("tn", dtype, 8, 8000, 1024, 1024, out=F32)["tile"] == tile
