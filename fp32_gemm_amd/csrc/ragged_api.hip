@@ -19,7 +19,7 @@ void set_last_hip_error(hipError_t e);  // sgemm_api.hip
 namespace {
 
 constexpr long long kMaxDim = 1LL << 30, kMaxStride = 1LL << 40, kMaxGroups = 1 << 16;
-constexpr long long kMaxGrid = 0x7FFFFFFFLL;
+constexpr double kMaxThreads = 4294967295.0;  // of a launch: HIP holds workgroups x threads in 32 bits
 constexpr long long kMaxIntegerK = 131071;  // 131071 * 128 * 128 < 2^31
 
 // Bytes of a rows x cols window, and whether two windows share any.
@@ -35,7 +35,7 @@ struct Plan {
   int shape;
   int bm, bn;
   bool longest_first;
-  long long grid;
+  long long grid;  // workgroups; 0: more than a launch holds
 };
 
 // What a tile costs, in microseconds as measured: a slice of 128 bytes of the
@@ -55,6 +55,13 @@ Plan plan(int form, int type, int out, int groups, long long M, long long N, lon
   constexpr double kUnits = 256, kLongSlices = 8;
   auto tiles = [](long long n, int t) { return (n + t - 1) / t; };
   const long long used = std::min<long long>(groups, M);
+  // Workgroups, as a double: queries may ask for more than 64 bits hold.
+  auto grid = [&](int bm, int bn) {
+    if (form == kFormTN) return groups * std::ceil(static_cast<double>(tiles(K, bm)) * tiles(N, bn) / 8) * 8;
+    // Every used group may leave one row tile partly filled; the dies take whole
+    // tiles, and partly filled ones kDeal columns at a time, in eights.
+    return static_cast<double>((M + used * (bm - 1)) / bm) * tiles(N, bn) + used * (kDeal - 1) + 8 + 8 * kDeal;
+  };
   const TileCost* cost = type == kElemF32 ? kCost32 : kCost16;
   const double steps = form == kFormTN ? static_cast<double>(M) / groups : static_cast<double>(K);
   const double slices = std::max(1.0, std::ceil(steps * elem_size(type) / 128));
@@ -63,6 +70,7 @@ Plan plan(int form, int type, int out, int groups, long long M, long long N, lon
   for (int shape = 0; shape < kShapes; ++shape) {
     if (!ragged_compiled(type, form, shape)) continue;
     const int bm = kRaggedRows[shape], bn = kRaggedCols[shape];
+    if (grid(bm, bn) * kRaggedThreads[shape] > kMaxThreads) continue;
     const TileCost& c = cost[shape];
     double count;  // tiles
     if (form == kFormTN) count = static_cast<double>(groups) * tiles(K, bm) * tiles(N, bn);
@@ -95,19 +103,17 @@ Plan plan(int form, int type, int out, int groups, long long M, long long N, lon
   }
   // Looking up the order of the lengths takes some 0.4 us of every tile.
   p.longest_first = form == kFormTN && slices >= kLongSlices;
+  if (best == 0) return Plan{};  // no tile's workgroups fit a launch
   p.bm = kRaggedRows[p.shape];
   p.bn = kRaggedCols[p.shape];
-  if (form == kFormTN) p.grid = groups * ((tiles(K, p.bm) * tiles(N, p.bn) + 7) / 8 * 8);
-  // Every used group may leave one row tile partly filled; the dies take whole
-  // tiles, and partly filled ones kDeal columns at a time, in eights.
-  else p.grid = (M + used * (p.bm - 1)) / p.bm * tiles(N, p.bn) + used * (kDeal - 1) + 8 + 8 * kDeal;
+  p.grid = static_cast<long long>(grid(p.bm, p.bn));
   return p;
 }
 
 int launch(int type, int form, const RaggedArgs& a, long long M, long long N, long long K,
            void* stream) {
   const Plan p = plan(form, type, a.out, a.groups, M, N, K);
-  if (p.grid > kMaxGrid) return SGEMM_ERR_UNSUPPORTED;
+  if (p.grid == 0) return SGEMM_ERR_UNSUPPORTED;
   RaggedArgs args = a;
   args.longest_first = p.longest_first;
   const int rc = sgemm_device_check();
@@ -313,7 +319,7 @@ int64_t gemm_grouped_plan(int32_t form, int32_t type, int32_t out_type, int32_t 
                           int64_t N, int64_t K, int32_t tile[2]) {
   if (tile == nullptr || !plan_arguments(form, type, out_type, groups, M, N, K)) return -1;
   const Plan p = plan(form, type, out_type, groups, M, N, K);
-  if (p.grid > kMaxGrid) return -1;
+  if (p.grid == 0) return -1;
   tile[0] = p.bm;
   tile[1] = p.bn;
   return p.grid;
@@ -322,7 +328,8 @@ int64_t gemm_grouped_plan(int32_t form, int32_t type, int32_t out_type, int32_t 
 int32_t gemm_grouped_tile(int32_t form, int32_t type, int32_t out_type, int32_t groups, int64_t M,
                           int64_t N, int64_t K) {
   if (!plan_arguments(form, type, out_type, groups, M, N, K)) return -1;
-  return plan(form, type, out_type, groups, M, N, K).shape;
+  const Plan p = plan(form, type, out_type, groups, M, N, K);
+  return p.grid == 0 ? -1 : p.shape;
 }
 
 int32_t gemm_grouped_tiles(int32_t form, int32_t type) {

@@ -923,6 +923,9 @@ using RaggedSlim = RaggedTile<16, 16, 1, 1, 4, 4, 128, 16, 2>;
 enum RaggedShape { kWide, kMid, kDeep, kSmall, kThin, kSlim, kShapes };
 constexpr int kRaggedRows[kShapes] = {256, 128, 128, 64, RaggedThin::BM, 16};  // of a tile
 constexpr int kRaggedCols[kShapes] = {256, 128, 128, 64, RaggedThin::BN, 16};
+constexpr int kRaggedThreads[kShapes] = {512, 512, 512, 256, 256, 256};
+static_assert(RaggedWide<kFormNT>::NT == 512 && RaggedMid::NT == 512 && RaggedDeep::NT == 512 &&
+              RaggedSmall<kFormNT>::NT == 256 && RaggedThin::NT == 256 && RaggedSlim::NT == 256, "threads");
 
 // The shapes that the plan may choose for a type and form, and no others, are
 // compiled.  Where rows of W are steps, few columns are short pieces of many

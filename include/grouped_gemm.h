@@ -47,8 +47,10 @@ extern "C" {
 #define GEMM_F16 2
 
 /* Limits (SGEMM_ERR_UNSUPPORTED beyond): M, N, K <= 2^30, leading dimensions
- * < 2^21, group strides <= 2^40, groups <= 65536, fewer than 2^31 tiles, and
- * K <= 131071 for igemm, whose 32-bit sums could pass their range there. */
+ * < 2^21, group strides <= 2^40, groups <= 65536, and K <= 131071 for igemm,
+ * whose 32-bit sums could pass their range there.  A launch holds fewer than
+ * 2^32 threads, which is 2^23 tiles of 256 x 256 outputs; the partly filled last
+ * tiles of a group count whole. */
 
 /* Y_r = alpha * X_r * W_e + beta * Y_r for every row r of every group e.
  * X is M x K, Y is M x N.  W_e = W + e * stride_w is K x N, or N x K when

@@ -127,3 +127,19 @@ def test_8_bit_products_in_every_tile(sizes, K, N):
         want[rows] = ((a[rows].double() @ b[e].double().t().contiguous()) * sa[rows, None].double() * sb[e].double()).float()
     fg.igemm(a, sa, b, sb, y, offsets=offsets_of(off))
     assert torch.equal(y, want)
+
+
+# ---- as many rows as there may be ----------------------------------------------------
+
+def test_a_thousand_million_rows():
+    # Tiles of 128 rows and 512 threads would take 2^32 threads.
+    M, K, N = 1 << 30, 8, 8
+    x = torch.zeros(M, K, dtype=BF16, device="cuda")
+    w = torch.arange(64, device="cuda").view(K, N).to(BF16)
+    y = torch.full((M, N), 7.0, dtype=BF16, device="cuda")
+    rows = torch.tensor([0, 1, 255, 256, (1 << 29) - 1, 1 << 29, M - 257, M - 2, M - 1], device="cuda")
+    x[rows] = whole(gen(5), (len(rows), K), BF16)
+    fg.gemm_grouped(x, w, None, y)
+    assert torch.equal(y[rows], (x[rows].double() @ w.double()).to(BF16))
+    y[rows] = 0
+    assert not y.view(torch.int64).any()
