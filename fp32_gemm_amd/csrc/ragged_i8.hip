@@ -41,12 +41,15 @@ __device__ __forceinline__ int code_of(float x, double inv) {
 // came, longer rows are read twice.  Memory-bound: bf16 8192 x 8192 in 38.6 us,
 // 5.2 TB/s, as a copy runs (59.6 with every code in 64 bits).
 constexpr int kQuantKeep = 8;
+// Workgroups in x; more rows go on in y (HIP holds 2^32 threads a dimension).
+constexpr int kQuantBlocks = 1 << 23;
 template <int ELEM, int THREADS>
 __global__ __launch_bounds__(256) void quantize_kernel(const char* x, long long ldx, signed char* q,
                                                        long long ldq, float* scale, int M, int K) {
   constexpr int ES = elem_size(ELEM), PER = 16 / ES;
   const int in = threadIdx.x % THREADS;
-  const long long row = static_cast<long long>(blockIdx.x) * (256 / THREADS) + threadIdx.x / THREADS;
+  const long long block = static_cast<long long>(blockIdx.y) * kQuantBlocks + blockIdx.x;
+  const long long row = block * (256 / THREADS) + threadIdx.x / THREADS;
   const bool live = row < M;
   const char* src = x + (live ? row : 0) * ldx * ES;
   signed char* dst = q + (live ? row : 0) * ldq;
@@ -135,7 +138,8 @@ hipError_t launch_quantize(const char* x, long long ldx, signed char* q, long lo
   // ones go to four waves.
   const int pieces = K / (16 / elem_size(ELEM));
   const bool wave = pieces <= 128 || (pieces <= 64 * kQuantKeep && M >= 4096);
-  const dim3 grid(static_cast<unsigned>(wave ? (M + 3) / 4 : M));
+  const unsigned blocks = static_cast<unsigned>(wave ? (M + 3) / 4 : M);
+  const dim3 grid(blocks < kQuantBlocks ? blocks : kQuantBlocks, (blocks + kQuantBlocks - 1) / kQuantBlocks);
   void* values[] = {&x, &ldx, &q, &ldq, &scale, &M, &K};
   return hipLaunchKernel(wave ? reinterpret_cast<const void*>(&quantize_kernel<ELEM, 64>)
                               : reinterpret_cast<const void*>(&quantize_kernel<ELEM, 256>),

@@ -143,3 +143,21 @@ def test_a_thousand_million_rows():
     assert torch.equal(y[rows], (x[rows].double() @ w.double()).to(BF16))
     y[rows] = 0
     assert not y.view(torch.int64).any()
+
+
+def test_quantising_more_rows_than_a_grid_dimension_holds():
+    # Past 2^26 rows, four to a workgroup of 256 threads, x alone would need 2^32.
+    M, K = (1 << 26) + 5, 8
+    x = torch.ones(M, K, dtype=BF16, device="cuda")
+    rows = torch.tensor([0, 3, 4, (1 << 25) - 1, 1 << 25, (1 << 25) + 1, (1 << 26) - 1, 1 << 26, M - 1], device="cuda")
+    x[rows] = torch.arange(1, 10, device="cuda").to(BF16)[:, None] * 2
+    x[rows, 0] = 0.5
+    q = torch.zeros(M, K, dtype=torch.int8, device="cuda")
+    s = torch.zeros(M, device="cuda")
+    fg.quantize_rows(x, q, s)
+    top = torch.arange(1, 10, device="cuda").double() * 2
+    want = torch.full((9, K), 127, dtype=torch.int8, device="cuda")
+    want[:, 0] = torch.round(127 * 0.5 / top).to(torch.int8)
+    assert torch.equal(q[rows], want) and torch.equal(s[rows], (top / 127).float())
+    q[rows], s[rows] = 127, 1.0 / 127
+    assert (q == 127).all() and (s == 1.0 / 127).all()
