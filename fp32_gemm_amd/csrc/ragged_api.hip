@@ -8,6 +8,7 @@
 
 #include "../../include/fp32_gemm.h"
 #include "../../include/grouped_gemm.h"
+#include "ragged_host_wave.hpp"
 #include "ragged_kernels.hpp"
 
 namespace fp32gemm {
@@ -48,29 +49,43 @@ constexpr TileCost kCost16[kShapes] = {{1.4, 1.4, 7.2, 8.5}, {.50, .64, 2.0, 2.5
 constexpr TileCost kCost32[kShapes] = {{7.1, 7.1, 8.5, 8.5}, {1.9, 1.93, 2.5, 2.5}, {1.95, 1.93, 3, 3},
                                        {.52, .62, .8, .8},   {.14, .22, .5, .5},    {.09, .11, .5, .5}};
 
-// The shape whose tiles, spread over the compute units, are done first by these
-// costs.  The offsets are on the device, so groups are taken as equal but for
-// the last row tile of each, which is half full.
-Plan plan(int form, int type, int out, int groups, long long M, long long N, long long K) {
-  constexpr double kUnits = 256, kLongSlices = 8;
-  auto tiles = [](long long n, int t) { return (n + t - 1) / t; };
+long long tiles(long long n, int t) { return (n + t - 1) / t; }
+
+// Workgroups of a shape for any split of the rows, as a double: queries may ask
+// for more than 64 bits hold.
+double workgroups(int form, int shape, int groups, long long M, long long N, long long K) {
+  const int bm = kRaggedRows[shape], bn = kRaggedCols[shape];
+  if (form == kFormTN) return groups * std::ceil(static_cast<double>(tiles(K, bm)) * tiles(N, bn) / 8) * 8;
+  // Every used group may leave one row tile partly filled; the dies take whole
+  // tiles, and partly filled ones kDeal columns at a time, in eights.
   const long long used = std::min<long long>(groups, M);
-  // Workgroups, as a double: queries may ask for more than 64 bits hold.
-  auto grid = [&](int bm, int bn) {
-    if (form == kFormTN) return groups * std::ceil(static_cast<double>(tiles(K, bm)) * tiles(N, bn) / 8) * 8;
-    // Every used group may leave one row tile partly filled; the dies take whole
-    // tiles, and partly filled ones kDeal columns at a time, in eights.
-    return static_cast<double>((M + used * (bm - 1)) / bm) * tiles(N, bn) + used * (kDeal - 1) + 8 + 8 * kDeal;
-  };
-  const TileCost* cost = type == kElemF32 ? kCost32 : kCost16;
+  return static_cast<double>((M + used * (bm - 1)) / bm) * tiles(N, bn) + used * (kDeal - 1) + 8 + 8 * kDeal;
+}
+
+// Slices of 128 bytes of a reduction; the offsets are on the device, so groups
+// are taken as equal.
+double slices_of(int form, int type, int groups, long long M, long long K) {
   const double steps = form == kFormTN ? static_cast<double>(M) / groups : static_cast<double>(K);
-  const double slices = std::max(1.0, std::ceil(steps * elem_size(type) / 128));
+  return std::max(1.0, std::ceil(steps * elem_size(type) / 128));
+}
+// Looking up the order of the lengths takes some 0.4 us of every tile.
+constexpr double kLongSlices = 8;
+bool longest_first(int form, double slices) { return form == kFormTN && slices >= kLongSlices; }
+
+// The shape whose tiles, spread over the compute units, are done first by these
+// costs.  Groups are taken as equal but for the last row tile of each, which is
+// half full.
+Plan plan(int form, int type, int out, int groups, long long M, long long N, long long K) {
+  constexpr double kUnits = 256;
+  const long long used = std::min<long long>(groups, M);
+  const TileCost* cost = type == kElemF32 ? kCost32 : kCost16;
+  const double slices = slices_of(form, type, groups, M, K);
   Plan p{};
   double best = 0;
   for (int shape = 0; shape < kShapes; ++shape) {
     if (!ragged_compiled(type, form, shape)) continue;
     const int bm = kRaggedRows[shape], bn = kRaggedCols[shape];
-    if (grid(bm, bn) * kRaggedThreads[shape] > kMaxThreads) continue;
+    if (workgroups(form, shape, groups, M, N, K) * kRaggedThreads[shape] > kMaxThreads) continue;
     const TileCost& c = cost[shape];
     double count;  // tiles
     if (form == kFormTN) count = static_cast<double>(groups) * tiles(K, bm) * tiles(N, bn);
@@ -101,13 +116,28 @@ Plan plan(int form, int type, int out, int groups, long long M, long long N, lon
       p.shape = shape;
     }
   }
-  // Looking up the order of the lengths takes some 0.4 us of every tile.
-  p.longest_first = form == kFormTN && slices >= kLongSlices;
+  p.longest_first = longest_first(form, slices);
   if (best == 0) return Plan{};  // no tile's workgroups fit a launch
   p.bm = kRaggedRows[p.shape];
   p.bn = kRaggedCols[p.shape];
-  p.grid = static_cast<long long>(grid(p.bm, p.bn));
+  p.grid = static_cast<long long>(workgroups(form, p.shape, groups, M, N, K));
   return p;
+}
+
+// The tile that workgroup w takes, as the kernel finds it.
+TileAt host_tile(int form, int shape, const Groups& g, int w, int K, int tiles_n, bool longest) {
+  const HostWave wave;
+  auto one = [&](auto bm) {
+    constexpr int BM = decltype(bm)::value;
+    return form == kFormTN ? tile_of_group<BM>(wave, g, w, static_cast<int>(tiles(K, BM)), tiles_n, longest)
+                           : tile_of_rows<BM>(wave, g, w, tiles_n);
+  };
+  switch (kRaggedRows[shape]) {
+    case 256: return one(std::integral_constant<int, 256>{});
+    case 128: return one(std::integral_constant<int, 128>{});
+    case 64: return one(std::integral_constant<int, 64>{});
+    default: return one(std::integral_constant<int, 16>{});
+  }
 }
 
 int launch(int type, int form, const RaggedArgs& a, long long M, long long N, long long K,
@@ -337,6 +367,26 @@ int32_t gemm_grouped_tiles(int32_t form, int32_t type) {
   int32_t bits = 0;
   for (int shape = 0; shape < kShapes; ++shape) bits |= ragged_compiled(type, form, shape) << shape;
   return bits;
+}
+
+int64_t gemm_grouped_tile_order(int32_t form, int32_t type, int32_t tile, int32_t groups,
+                                const int32_t* offsets, int64_t M, int64_t N, int64_t K, int64_t first,
+                                int64_t count, int32_t* order) {
+  if (!plan_arguments(form, type, GEMM_F32, groups, M, N, K) || tile < 0 || tile >= kShapes ||
+      !ragged_compiled(type, form, tile) || (offsets == nullptr && groups != 1) || first < 0 || count < 0 ||
+      (count > 0 && order == nullptr))
+    return -1;
+  const double grid = M == 0 && form != kFormTN ? 0 : workgroups(form, tile, groups, M, N, K);
+  if (grid * kRaggedThreads[tile] > kMaxThreads) return -1;
+  const Groups g{offsets, groups, static_cast<int>(M)};
+  const bool longest = longest_first(form, slices_of(form, type, groups, M, K));
+  for (int64_t w = first; w < std::min<int64_t>(first + count, grid); ++w) {
+    const TileAt at = host_tile(form, tile, g, static_cast<int>(w), static_cast<int>(K),
+                                static_cast<int>(tiles(N, kRaggedCols[tile])), longest);
+    const int32_t four[4] = {at.group, at.row, at.hi, at.n};
+    std::copy(four, four + 4, order + 4 * (w - first));
+  }
+  return static_cast<int64_t>(grid);
 }
 
 const char* gemm_grouped_status_string(int status) {

@@ -27,6 +27,8 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "ragged_order.hpp"
+
 namespace fp32gemm {
 
 enum Elem { kElemF32 = 0, kElemBF16 = 1, kElemF16 = 2, kElemI8 = 3 };
@@ -65,7 +67,6 @@ struct RaggedTile {
   static constexpr int NT = WAVES * WAVES_K * 64;
   static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
   static constexpr int FM = WM / MF, FN = WN / MF;         // blocks of a wave
-  static constexpr int BAND = BM >= 256 ? 4 : 8;           // row tiles that share operands
   static constexpr int STAGE = (BM + BN) * SL;             // bytes of a slice
   static constexpr int RING = STAGE * S * WAVES_K;
   static constexpr int SUMS = (WAVES_K - 1) * BM * BN * 4; // partial sums at the end
@@ -308,175 +309,6 @@ __device__ __forceinline__ void ragged_barrier() {
 }
 
 // ---------------------------------------------------------------------------
-// Rows of group e, whatever the offsets hold: within 0 .. rows, never negative.
-struct RowSpan { int lo, hi; };
-__device__ __forceinline__ RowSpan group_rows(const RaggedArgs& p, int e) {
-  if (p.offsets == nullptr) return {0, p.rows};
-  const int lo = min(max(p.offsets[e], 0), p.rows);
-  return {lo, min(max(p.offsets[e + 1], lo), p.rows)};
-}
-
-// The sum over this and all lower lanes.
-__device__ __forceinline__ int wave_sum_below(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // from 1, 2, 4 and 8 lanes below,
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);  // within rows of sixteen,
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // a row's last lane to the next row,
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // and lane 31 to the upper half
-  return v;
-}
-
-// Consecutive workgroups run on the eight dies in turn, each with its own L2:
-// die x takes the x-th run of consecutive tiles.  Returns -1 past the last.
-__device__ __forceinline__ int die_order(int w, int tiles) {
-  const int x = w & 7, i = w >> 3, q = tiles >> 3, r = tiles & 7;
-  return i < q + (x < r) ? x * q + min(x, r) + i : -1;
-}
-
-// Within a group, tiles go down BAND row tiles before the next column, so that
-// tiles in flight on a die share operand rows and columns in its L2.
-struct TileRow { int m, n; };
-template <int BAND>
-__device__ __forceinline__ TileRow band_order(int id, int tm, int tn) {
-  const int band = id / (BAND * tn), first = band * BAND, rows = min(BAND, tm - first);
-  const int in = id - first * tn;
-  return {first + in % rows, in / rows};
-}
-
-// The tile of workgroup w: its group, first row, the group's end and its
-// column; group -1 past the last.  Group after group, the last row tile of each
-// partly filled.  A lane counts a group, 64 at a time.
-struct TileAt { int group, row, hi, n; };
-template <int BM, int BAND>
-__device__ __forceinline__ TileAt tile_in_order(const RaggedArgs& p, int w, int tiles_n, int lane) {
-  RowSpan s{0, 0};
-  int before = 0, upto = 0, n = 0, e0 = 0;
-  auto count = [&] {
-    s = e0 + lane < p.groups ? group_rows(p, e0 + lane) : RowSpan{0, 0};
-    n = (s.hi - s.lo + BM - 1) / BM;
-    upto = before + wave_sum_below(n);
-  };
-  for (;; e0 += 64) {
-    count();
-    if (e0 + 64 >= p.groups) break;
-    before = __builtin_amdgcn_readlane(upto, 63);
-  }
-  const int id = die_order(w, __builtin_amdgcn_readlane(upto, 63) * tiles_n);
-  if (id < 0) return {-1, 0, 0, 0};
-  const int want = id / tiles_n;  // the group's row tiles include the want-th of all
-  if (p.groups > 64) {
-    for (e0 = 0, before = 0;; e0 += 64) {
-      count();
-      const int end = __builtin_amdgcn_readlane(upto, 63);
-      if (end > want) break;
-      before = end;
-    }
-  }
-  const int l = __builtin_ctzll(__ballot(upto > want)), tm = __builtin_amdgcn_readlane(n, l);
-  const TileRow at = band_order<BAND>(id - (__builtin_amdgcn_readlane(upto, l) - tm) * tiles_n, tm, tiles_n);
-  return {e0 + l, __builtin_amdgcn_readlane(s.lo, l) + at.m * BM, __builtin_amdgcn_readlane(s.hi, l), at.n};
-}
-
-// The same for tiles whose time goes by their filled part.  Whole row tiles
-// come first.  The rows that are left of each group make partly filled tiles,
-// which take less time the fewer blocks of CLASS rows they hold; they come
-// last, the fullest first, so that the workgroups that finish early fill up
-// with the short ones.  The dies take them in turn, kDeal columns at a time,
-// which share the rows.
-constexpr int kDeal = 4;
-template <int BM, int CLASS, int BAND>
-__device__ __forceinline__ TileAt tile_by_fill(const RaggedArgs& p, int w, int tiles_n, int lane) {
-  constexpr int NC = BM / CLASS;
-  const int x = w & 7, i = w >> 3;
-  RowSpan s{0, 0};
-  int whole = 0, upto = 0;             // whole row tiles of the lane's group, and of all up to it
-  unsigned long long members[NC];      // groups with c + 1 started blocks left
-  int wholes = 0, parts[NC] = {};      // in the chunks before, and after the first pass in all
-  int e0 = 0;
-  auto count = [&] {
-    s = e0 + lane < p.groups ? group_rows(p, e0 + lane) : RowSpan{0, 0};
-    const int n = s.hi - s.lo, left = (n % BM + CLASS - 1) / CLASS;
-    whole = n / BM;
-    upto = wave_sum_below(whole);
-#pragma unroll
-    for (int c = 0; c < NC; ++c) members[c] = __ballot(left == c + 1);
-  };
-  for (;; e0 += 64) {
-    count();
-    wholes += __builtin_amdgcn_readlane(upto, 63);
-#pragma unroll
-    for (int c = 0; c < NC; ++c) parts[c] += __builtin_popcountll(members[c]);
-    if (e0 + 64 >= p.groups) break;
-  }
-  const int here = wholes * tiles_n / 8 + (x < wholes * tiles_n % 8);  // whole tiles of this die
-  const bool in_whole = i < here;
-  int id, want, n, kind = 0;  // the row tile among the whole ones, or among those of class `kind`
-  if (in_whole) {
-    id = die_order(w, wholes * tiles_n);
-    want = id / tiles_n;
-    n = 0;
-  } else {
-    const int deals = (tiles_n + kDeal - 1) / kDeal;  // of a row tile
-    id = (i - here) / kDeal * 8 + (7 - x);
-    want = id / deals;
-    n = id % deals * kDeal + (i - here) % kDeal;
-    for (kind = NC - 1; kind >= 0; --kind) {
-      int all = 0;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) all = c == kind ? parts[c] : all;
-      if (want < all) break;
-      want -= all;
-    }
-    if (kind < 0 || n >= tiles_n) return {-1, 0, 0, 0};
-  }
-  unsigned long long hit;
-  int before = 0;
-  auto look = [&] {  // the lane whose group holds the tile, counting this chunk's from `before`
-    unsigned long long m = 0;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) m = c == kind ? members[c] : m;
-    const int rank = before + __builtin_amdgcn_mbcnt_hi(
-        static_cast<unsigned>(m >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<unsigned>(m), 0));
-    hit = in_whole ? __ballot(before + upto > want) : __ballot((m >> lane & 1) && rank == want);
-    return in_whole ? __builtin_amdgcn_readlane(upto, 63) : __builtin_popcountll(m);
-  };
-  if (p.groups <= 64) {
-    look();
-  } else {
-    for (e0 = 0;; e0 += 64) {
-      count();
-      const int these = look();
-      if (hit != 0 || e0 + 64 >= p.groups) break;
-      before += these;
-    }
-  }
-  const int l = __builtin_ctzll(hit), tm = __builtin_amdgcn_readlane(whole, l);
-  int row = tm;
-  if (in_whole) {
-    const TileRow at = band_order<BAND>(
-        id - (before + __builtin_amdgcn_readlane(upto, l) - tm) * tiles_n, tm, tiles_n);
-    row = at.m;
-    n = at.n;
-  }
-  return {e0 + l, __builtin_amdgcn_readlane(s.lo, l) + row * BM, __builtin_amdgcn_readlane(s.hi, l), n};
-}
-
-// The group whose length is the `rank`-th largest (the lower one of equals), so
-// that the longest reductions start first.  Past 64 groups: as they come.
-__device__ __forceinline__ int by_length(const RaggedArgs& p, int rank, int lane) {
-  if (p.groups > 64) return rank;
-  const RowSpan s = lane < p.groups ? group_rows(p, lane) : RowSpan{0, -1};
-  const int n = s.hi - s.lo;
-  int above = 0;
-  for (int e = 0; e < p.groups; ++e) {
-    const int o = __builtin_amdgcn_readlane(n, e);
-    above += o > n || (o == n && e < lane);
-  }
-  return __builtin_ctzll(__ballot(lane < p.groups && above == rank));
-}
-
-// ---------------------------------------------------------------------------
 template <int ELEM, int FORM, class T>
 __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const RaggedArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the stub alone and lacks the matrix builtins
@@ -498,16 +330,15 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
   long long row_c;
   const char *a, *b;
   int n0, m_bytes = 0;  // the tile's first column of B, and byte of a step's row of A
+  const DeviceWave look{lane};
+  const Groups groups{p.offsets, p.groups, p.rows};
   if constexpr (FORM == kFormTN) {
-    // Each group's tiles are dealt out over all dies: groups differ in length.
-    const int tiles_m = (p.M + T::BM - 1) / T::BM, each = tiles_m * tiles_n, room = (each + 7) & ~7;
-    group = blockIdx.x / room;
-    if (p.longest_first) group = by_length(p, group, lane);
-    const int id = die_order(blockIdx.x % room, each);
-    if (id < 0) return;
-    const TileRow at = band_order<T::BAND>(id, tiles_m, tiles_n);
-    const RowSpan s = group_rows(p, group);
-    const int m0 = at.m * T::BM;
+    const TileAt at =
+        tile_of_group<T::BM>(look, groups, blockIdx.x, (p.M + T::BM - 1) / T::BM, tiles_n, p.longest_first);
+    group = at.group;
+    if (group < 0) return;
+    const RowSpan s = groups.span(group);
+    const int m0 = at.row * T::BM;
     m_bytes = m0 * ES;
     n0 = at.n * T::BN;
     rows = min(T::BM, p.M - m0);
@@ -516,9 +347,7 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
     b = p.B + s.lo * p.ldb + static_cast<long long>(n0) * ES;
     row_c = m0;
   } else {
-    TileAt at;
-    if constexpr (T::BM == 256) at = tile_by_fill<T::BM, T::BM / 4, T::BAND>(p, blockIdx.x, tiles_n, lane);
-    else at = tile_in_order<T::BM, T::BAND>(p, blockIdx.x, tiles_n, lane);
+    const TileAt at = tile_of_rows<T::BM>(look, groups, blockIdx.x, tiles_n);
     group = at.group;
     n0 = at.n * T::BN;
     rows = min(T::BM, at.hi - at.row);

@@ -28,6 +28,7 @@ _SIGS = {
     "gemm_grouped_plan": ([_i32, _i32, _i32, _i32, _i64, _i64, _i64, ctypes.POINTER(_i32)], _i64),
     "gemm_grouped_tile": ([_i32, _i32, _i32, _i32, _i64, _i64, _i64], _i32),
     "gemm_grouped_tiles": ([_i32, _i32], _i32),
+    "gemm_grouped_tile_order": ([_i32, _i32, _i32, _i32, _vp, _i64, _i64, _i64, _i64, _i64, _vp], _i64),
     "gemm_grouped_status_string": ([ctypes.c_int], ctypes.c_char_p),
 }
 for _name, (_args, _res) in _SIGS.items():
@@ -76,6 +77,22 @@ def tiles(form: str, dtype) -> list:
     if bits < 0:
         raise ValueError("bad arguments")
     return [name for i, name in enumerate(TILES) if bits >> i & 1]
+
+
+def tile_order(form: str, dtype, tile: str, offsets, M: int, N: int, K: int, first=0, count=None) -> list:
+    """(group, first row, end of the group's rows, column) of each workgroup's
+    tile, group -1 where it has none; offsets is a list, or None for one group of
+    M rows.  For weight gradients the first row is the row tile and the end 0."""
+    at = None if offsets is None else (_i32 * len(offsets))(*offsets)
+    groups = 1 if offsets is None else len(offsets) - 1
+    args = (_FORMS[form], {**_TYPES, **_INT8}[dtype], TILES.index(tile), groups, at, M, N, K, first)
+    n = _lib.gemm_grouped_tile_order(*args, 0, None)
+    if n < 0:
+        raise ValueError("bad arguments")
+    count = max(0, n - first) if count is None else min(count, max(0, n - first))
+    order = (_i32 * (4 * count))()
+    _lib.gemm_grouped_tile_order(*args, count, order)
+    return [tuple(order[4 * i:4 * i + 4]) for i in range(count)]
 
 
 def gemm_grouped(X, W, offsets, Y, alpha=1.0, beta=0.0, transpose_w=False, stream=None):

@@ -119,6 +119,16 @@ int32_t gemm_grouped_tile(int32_t form, int32_t type, int32_t out_type, int32_t 
  * arguments out of range. */
 int32_t gemm_grouped_tiles(int32_t form, int32_t type);
 
+/* Which outputs each workgroup computes with the tile of index `tile`, without a
+ * device: `offsets` is a HOST array here (NULL: one group).  For workgroups
+ * first .. first + count - 1 of the launch, order[4 i ..] gets the group (-1:
+ * none), the first row (form 2: the row tile), the end of the group's rows
+ * (form 2: 0) and the tile's column.  Returns the number of workgroups, or -1
+ * for arguments out of range or more workgroups than a launch holds. */
+int64_t gemm_grouped_tile_order(int32_t form, int32_t type, int32_t tile, int32_t groups,
+                                const int32_t* offsets, int64_t M, int64_t N, int64_t K, int64_t first,
+                                int64_t count, int32_t* order);
+
 /* Static string for a status of these calls (never NULL). */
 const char* gemm_grouped_status_string(int status);
 

@@ -60,3 +60,72 @@ def test_what_no_launch_holds_is_unsupported():
     K = N = 1 << 20
     assert grouped._lib.gemm_grouped_wgrad(bf16, bf16, 65536, 1 << 39, 16, N, K, 1.0, far[0], K, far[1], N, 0.0,
                                            far[2], N, N * K, None) == 5
+
+
+# ---- the order of the tiles, by the kernels' own code on the host ---------------------
+
+ROWS = {"256x256": 256, "128x128": 128, "128x128 deep": 128, "64x64": 64, "16x32": 16, "16x16": 16}
+COLS = {"256x256": 256, "128x128": 128, "128x128 deep": 128, "64x64": 64, "16x32": 32, "16x16": 16}
+
+
+def splits(bm):
+    """Groups' lengths: each with one row more than whole tiles (the most tiles
+    there can be), each with only a part of a tile, single rows, gaps, more groups
+    than the 64 that a wave looks at together, and ordinary ones."""
+    import random
+    r = random.Random(bm)
+    yield [1]
+    yield [bm + 1] * 3
+    yield [1] * 7
+    yield [0, 0, 5, 0]
+    yield [2 * bm + 1, 1, bm + 1, 0, 1]
+    yield [1, 0] * 40
+    yield [bm * (i % 3) + 1 for i in range(70)]
+    yield [r.randrange(1, bm) for _ in range(150)]
+    for groups in (2, 9, 64, 65, 129):
+        yield [r.choice((0, 1, r.randrange(3 * bm), bm * r.randrange(3))) for _ in range(groups)]
+
+
+@pytest.mark.parametrize("tile", ["256x256", "128x128", "64x64", "16x32", "16x16"])
+@pytest.mark.parametrize("tiles_n", [1, 2, 3, 5, 12])
+def test_every_output_tile_has_one_workgroup(tile, tiles_n):
+    bm, N = ROWS[tile], COLS[tile] * (tiles_n - 1) + 1
+    for sizes in splits(bm):
+        off = [0]
+        for n in sizes:
+            off.append(off[-1] + n)
+        order = grouped.tile_order("nt", BF16, tile, off, off[-1], N, 64)
+        got = sorted(t for t in order if t[0] >= 0)
+        want = sorted((e, row, off[e + 1], n) for e in range(len(sizes)) for row in range(off[e], off[e + 1], bm)
+                      for n in range(tiles_n))
+        assert got == want
+
+
+@pytest.mark.parametrize("tile", ["256x256", "128x128 deep", "64x64"])
+@pytest.mark.parametrize("K,N", [(1, 1), (700, 300), (513, 1025)])
+def test_every_weight_gradient_tile_has_one_workgroup(tile, K, N):
+    for sizes in ([3000, 1, 0, 900, 3000], [0], [10] * 70, list(range(600, 664))):
+        off = [0]
+        for n in sizes:
+            off.append(off[-1] + n)
+        order = grouped.tile_order("tn", BF16, tile, off, off[-1], N, K)
+        up = lambda n, t: -(-n // t)  # noqa: E731
+        want = sorted((e, m, 0, n) for e in range(len(sizes)) for m in range(up(K, ROWS[tile]))
+                      for n in range(up(N, COLS[tile])))
+        assert sorted(t for t in order if t[0] >= 0) == want
+        if len(sizes) <= 64 and sum(sizes) / len(sizes) >= 512:  # long: the longest first
+            lengths = [sizes[t[0]] for t in order if t[0] >= 0]
+            assert lengths == sorted(lengths, reverse=True)
+
+
+def test_one_group_of_all_rows():
+    order = grouped.tile_order("nn", F32, "64x64", None, 130, 70, 64)
+    assert sorted(t for t in order if t[0] >= 0) == sorted((0, m, 130, n) for m in (0, 64, 128) for n in (0, 1))
+
+
+def test_tile_order_refusals():
+    for bad in (dict(tile="16x16", form="nn"), dict(offsets=[0]), dict(M=-1), dict(M=1 << 30, tile="16x16")):
+        args = dict(form="nt", dtype=BF16, tile="64x64", offsets=[0, 5], M=5, N=64, K=64, **{})
+        args.update(bad)
+        with pytest.raises(ValueError):
+            grouped.tile_order(**args)
