@@ -351,8 +351,7 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
     group = at.group;
     n0 = at.n * T::BN;
     rows = min(T::BM, at.hi - at.row);
-    // Offsets out of order may count more tiles than an int holds.
-    if (group < 0 || group >= p.groups || at.row < 0 || rows <= 0) return;
+    if (group < 0) return;
     len = p.K;
     a = p.A + at.row * p.lda;
     b = p.B + group * p.stride_b + (B_ALONG ? n0 * p.ldb : static_cast<long long>(n0) * ES);

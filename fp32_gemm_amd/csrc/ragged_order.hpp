@@ -25,6 +25,15 @@ struct Groups {
     const int lo = inside(offsets[e], 0);
     return {lo, inside(offsets[e + 1], lo)};
   }
+  // The most tiles of bm rows there are when the groups follow one another.
+  // Offsets out of order may count more; such a launch computes nothing, so that
+  // every tile found is one of a group's.  No sum passes an int on the way: a
+  // launch has fewer than 2^24 workgroups, hence whole tiles of all rows, and 64
+  // groups hold all rows 32 times at most, as the step back between two times
+  // is an empty group.
+  __host__ __device__ __forceinline__ int most(int bm) const {
+    return rows / bm + (groups < rows ? groups : rows);
+  }
 };
 
 struct DeviceWave {
@@ -91,10 +100,11 @@ __host__ __device__ __forceinline__ TileAt tile_in_order(const W& wave, const Gr
   };
   for (;; e0 += 64) {
     count();
-    if (e0 + 64 >= p.groups) break;
     before = wave.at(upto, 63);
+    if (before > p.most(BM)) return {-1, 0, 0, 0};
+    if (e0 + 64 >= p.groups) break;
   }
-  const int id = die_order(w, wave.at(upto, 63) * tiles_n);
+  const int id = die_order(w, before * tiles_n);
   if (id < 0) return {-1, 0, 0, 0};
   const int want = id / tiles_n;  // the group's row tiles include the want-th of all
   if (p.groups > 64) {
@@ -137,6 +147,7 @@ __host__ __device__ __forceinline__ TileAt tile_by_fill(const W& wave, const Gro
   for (;; e0 += 64) {
     count();
     wholes += wave.at(upto, 63);
+    if (wholes > p.most(BM)) return {-1, 0, 0, 0};
 #pragma unroll
     for (int c = 0; c < NC; ++c) parts[c] += __builtin_popcountll(members[c]);
     if (e0 + 64 >= p.groups) break;

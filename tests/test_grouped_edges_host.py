@@ -129,3 +129,30 @@ def test_tile_order_refusals():
         args.update(bad)
         with pytest.raises(ValueError):
             grouped.tile_order(**args)
+
+
+@pytest.mark.parametrize("tile", ["256x256", "128x128", "64x64", "16x32", "16x16"])
+def test_offsets_out_of_order_never_leave_the_operands(tile):
+    # Every tile is one of a group's: rows inside the group, columns inside N. Where
+    # the groups count more whole tiles than the rows can have tiles, there is none at
+    # all: sums would pass 32 bits (65536 groups of which every other one holds all).
+    import random
+    r = random.Random(ROWS[tile])
+    for M in (5, 1000, 1 << 20, 150000001):
+        for groups in (3, 64, 65, 1000, 65536):
+            for tiles_n in (1, 3):
+                if M // ROWS[tile] * tiles_n > 1 << 23:
+                    continue  # more than a launch holds
+                kinds = [[0 if e % 2 == 0 else M for e in range(groups + 1)],
+                         [r.choice((-5, 0, M // 2, M, 1 << 30, r.randrange(M))) for _ in range(groups + 1)]]
+                for off in kinds:
+                    span = lambda e: (min(max(off[e], 0), M), min(max(off[e + 1], min(max(off[e], 0), M)), M))  # noqa: E731
+                    whole = sum((hi - lo) // ROWS[tile] for lo, hi in map(span, range(groups)))
+                    args = ("nt", BF16, tile, off, M, tiles_n * COLS[tile], 64)
+                    for first in (0, r.randrange(1 << 16), 1 << 19):
+                        for e, row, end, n in grouped.tile_order(*args, first, 64):
+                            if e < 0:
+                                continue
+                            lo, hi = span(e)
+                            assert 0 <= n < tiles_n and lo <= row < hi == end and (row - lo) % ROWS[tile] == 0
+                            assert whole <= M // ROWS[tile] + min(groups, M)
