@@ -161,3 +161,118 @@ def test_quantising_more_rows_than_a_grid_dimension_holds():
     assert torch.equal(q[rows], want) and torch.equal(s[rows], (top / 127).float())
     q[rows], s[rows] = 127, 1.0 / 127
     assert (q == 127).all() and (s == 1.0 / 127).all()
+
+
+# ---- wrong offsets, bad values ---------------------------------------------------------
+
+def guarded(rows, cols, dtype, fill):
+    """A rows x cols view amid `fill`, its rows 8 elements more than cols apart."""
+    base = torch.full((rows + 4, cols + 8), fill, device="cuda").to(dtype)
+    return base, base[2:2 + rows, :cols]
+
+
+WRONG = [[50, 20, -7, 300, 10], [-5, 1000, -1000, 1 << 30, -(1 << 30)], [100, 100, 0, 0, 100], [0, 90, 30, 60, 2000]]
+
+
+def spans_of_wrong(off, M):
+    out = []
+    for e in range(len(off) - 1):
+        lo = min(max(off[e], 0), M)
+        out.append(slice(lo, min(max(off[e + 1], lo), M)))
+    return out
+
+
+MANY_WRONG = [[0 if e % 2 else 4000 for e in range(151)],  # more tiles than the rows can have: nothing is computed
+              [-5 if e == 0 else 26 * (e + (e == 70) - (e == 71)) for e in range(151)]]
+
+
+@pytest.mark.parametrize("off", WRONG + MANY_WRONG)
+@pytest.mark.parametrize("M,K,N", [(100, 64, 64), (4000, 72, 1100), (4000, 72, 3600)])
+@pytest.mark.parametrize("dtype,trans", [(BF16, True), (BF16, False), (F32, False), (torch.int8, True)])
+def test_wrong_offsets_write_products_of_their_own_rows(off, M, K, N, dtype, trans):
+    # Whatever the offsets hold, an output is left alone or the product of its own
+    # row of X and some group's weights; what surrounds the operands (NaN, or codes
+    # that no product has) neither enters nor changes.
+    g = gen(20)
+    E = len(off) - 1
+    if N == 3600:
+        assert fg.grouped.plan("nt" if trans else "nn", dtype, E, M, N, K, out=F32)["BM"] == 256
+    _, x = guarded(M, K, dtype, 99 if dtype is torch.int8 else float("nan"))
+    x.copy_(whole(g, (M, K), dtype))
+    _, w2 = guarded(E * (N if trans else K), K if trans else N, dtype, 99 if dtype is torch.int8 else float("nan"))
+    w = w2.unflatten(0, (E, N if trans else K))
+    w.copy_(whole(g, tuple(w.shape), dtype))
+    yb, y = guarded(M, N, F32, 7777.0)
+    before = yb.clone()
+    if dtype is torch.int8:
+        one = torch.ones(E, N, device="cuda")
+        fg.igemm(x, torch.ones(M, device="cuda"), w, one, y, offsets=offsets_of(off))
+    else:
+        fg.gemm_grouped(x, w, offsets_of(off), y, transpose_w=trans)
+    known = y == 7777.0
+    for e in range(E):
+        we = w[e].float()
+        known |= y == x.float() @ (we.t().contiguous() if trans else we)
+    assert known.all()
+    if off in (WRONG[0], WRONG[3], MANY_WRONG[1]):  # no more tiles than rows in order could have
+        assert (y != 7777.0).any()
+    y.copy_(before[2:2 + M, :N])
+    assert torch.equal(yb, before)
+
+
+@pytest.mark.parametrize("off", WRONG)
+@pytest.mark.parametrize("dtype,K,N", [(BF16, 72, 100), (F32, 72, 100), (F16, 1000, 1030), (F32, 1000, 1030)])
+def test_weight_gradients_of_wrong_offsets(off, dtype, K, N):
+    g = gen(21)
+    M, E = 1500, len(off) - 1
+    _, x = guarded(M, K, dtype, float("nan"))
+    _, dy = guarded(M, N, dtype, float("nan"))
+    x.copy_(whole(g, (M, K), dtype))
+    dy.copy_(whole(g, (M, N), dtype))
+    wb, w2 = guarded(E * K, N, F32, 7777.0)
+    before = wb.clone()
+    dw = w2.unflatten(0, (E, K))
+    fg.gemm_grouped_wgrad(x, dy, offsets_of(off), dw)
+    for e, rows in enumerate(spans_of_wrong(off, M)):
+        assert torch.equal(dw[e], (x[rows].double().t().contiguous() @ dy[rows].double()).float())
+    w2.copy_(before[2:2 + E * K, :N])
+    assert torch.equal(wb, before)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("sizes,K,N", [([40, 25], 160, 96), ([40, 25], 161, 97), ([600, 700], 161, 2100)])
+def test_bad_values_stay_in_their_rows_and_columns_with_transposed_weights(dtype, sizes, K, N):
+    g = gen(22)
+    off, M = layout(sizes)
+    x, w = whole(g, (M, K), dtype), whole(g, (2, N, K), dtype)
+    w[w == 0] = 1
+    x[7, 3], x[50, K - 1], w[1, 11, K - 1], w[0, N - 1, 0] = float("nan"), float("inf"), float("nan"), -float("inf")
+    x[off[1] - 1, K - 1] = float("inf")
+    y = torch.full((M, N), 7.0, device="cuda", dtype=F32)
+    want = y.clone()
+    for e, rows in enumerate(spans(off)):
+        want[rows] = (x[rows].double() @ w[e].double().t().contiguous()).float()
+    fg.gemm_grouped(x, w, offsets_of(off), y, transpose_w=True)
+    assert torch.equal(torch.isnan(y), torch.isnan(want))
+    fine = ~torch.isnan(want)
+    assert torch.equal(y[fine], want[fine])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("K,N", [(72, 96), (73, 97), (1000, 1030)])
+def test_bad_values_stay_in_their_group_row_and_column_of_weight_gradients(dtype, K, N):
+    # A bad token spoils its own group's weights: one row of dW by X, one column by
+    # dY. Rows that no group owns, in front and behind, spoil nothing.
+    g = gen(23)
+    off, M = layout([130, 0, 257])
+    x, dy = whole(g, (M, K), dtype), whole(g, (M, N), dtype)
+    for t in (x, dy):
+        t[t == 0] = 1
+        t[0], t[-2:] = float("nan"), float("inf")
+    x[5, 3], x[140, K - 1], dy[130, 2], dy[M - 3, N - 1] = float("nan"), float("inf"), float("inf"), float("nan")
+    dw = torch.full((3, K, N), 7.0, device="cuda")
+    fg.gemm_grouped_wgrad(x, dy, offsets_of(off), dw)
+    want = torch.stack([x[rows].double().t().contiguous() @ dy[rows].double() for rows in spans(off)]).float()
+    assert torch.equal(torch.isnan(dw), torch.isnan(want))
+    fine = ~torch.isnan(want)
+    assert torch.equal(dw[fine], want[fine])
