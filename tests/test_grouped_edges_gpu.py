@@ -214,7 +214,7 @@ def test_wrong_offsets_write_products_of_their_own_rows(off, M, K, N, dtype, tra
         we = w[e].float()
         known |= y == x.float() @ (we.t().contiguous() if trans else we)
     assert known.all()
-    if off in (WRONG[0], WRONG[3], MANY_WRONG[1]):  # no more tiles than rows in order could have
+    if off in (WRONG[0], WRONG[2], MANY_WRONG[1]):  # no more tiles than groups in order can have
         assert (y != 7777.0).any()
     y.copy_(before[2:2 + M, :N])
     assert torch.equal(yb, before)
