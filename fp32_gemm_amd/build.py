@@ -5,7 +5,9 @@ translation units; each candidate passes through the C++ legality checker at
 compile time and only legal ones instantiate kernels.  The units compile in
 parallel with hipcc and link into ``fp32_gemm_amd/libfp32_gemm_amd.so``.  The
 compiler's per-kernel resource report (VGPRs, AGPRs, scratch, occupancy) is
-saved to ``fp32_gemm_amd/_build/resources.json``.
+saved to ``fp32_gemm_amd/_build/resources.json``.  Where torch's C++ headers and
+g++ are found, ``_torch_calls.so``, the module of the grouped products' Python
+calls, is built beside the library.
 
 Usage: ``python -m fp32_gemm_amd.build`` (or ``__graft_entry__.build()``).
 """
@@ -385,7 +387,6 @@ def build(verbose=True, jobs=None):
             if m and v.get("ScratchSize", 0) > 0:
                 new.add(tuple(int(x) for x in m.groups()[:12]))
         if not new:
-            _build_calls()
             return LIB
         bad = sorted(_spilling() | new)
         with open(SPILLING, "w") as f:
@@ -426,9 +427,25 @@ def _build_once(verbose, jobs):
     return resources
 
 
-def _build_calls():
+def missing_for_calls():
+    """What build_calls() needs and this machine lacks, or None."""
+    import importlib.util
+    if importlib.util.find_spec("torch") is None:
+        return "torch"
+    import torch
+    if not os.path.exists(os.path.join(os.path.dirname(torch.__file__), "include", "torch", "csrc", "autograd",
+                                       "python_variable.h")):
+        return "torch's C++ headers"
+    return None if shutil.which("g++") else "g++"
+
+
+def build_calls():
     """The module that checks tensors and calls the library for grouped.py:
-    host code against torch's headers, linked to the library beside it."""
+    host code against torch's headers, linked to the library beside it, which
+    build() makes.  The C ABI does without it."""
+    lacking = missing_for_calls()
+    if lacking:
+        raise RuntimeError(f"{os.path.basename(CALLS)}: {lacking} not found")
     import sysconfig
 
     import torch
@@ -455,5 +472,14 @@ def clean():
             os.remove(built)
 
 
-if __name__ == "__main__":
+def main():
     build(verbose="-q" not in sys.argv)
+    lacking = missing_for_calls()
+    if lacking:
+        print(f"[build] {lacking} not found: the library is built, the Python calls of grouped.py are not", flush=True)
+    else:
+        build_calls()
+
+
+if __name__ == "__main__":
+    main()
