@@ -453,6 +453,7 @@ def build_calls():
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
     tmp = CALLS + ".tmp%d" % os.getpid()
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           f'-DBUILT_FOR_TORCH="{torch.__version__}"',
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
     cmd += [f"-I{p}" for p in (*cpp_extension.include_paths(), os.path.join(rocm, "include"),
                                sysconfig.get_paths()["include"])]

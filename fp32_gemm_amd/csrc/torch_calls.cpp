@@ -263,4 +263,18 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, kMeth
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__torch_calls() { return PyModule_Create(&kModule); }
+// torch's C++ interface differs between versions: only the one this was
+// compiled against may load it.
+PyMODINIT_FUNC PyInit__torch_calls() {
+  PyObject* const torch = PyImport_ImportModule("torch");
+  PyObject* const held = torch ? PyObject_GetAttrString(torch, "__version__") : nullptr;
+  PyObject* const version = held ? PyObject_Str(held) : nullptr;
+  const char* const text = version ? PyUnicode_AsUTF8(version) : nullptr;
+  const bool same = text && std::string(text) == BUILT_FOR_TORCH;
+  if (text && !same)
+    PyErr_Format(PyExc_ImportError, "built for torch " BUILT_FOR_TORCH ", this is torch %s", text);
+  Py_XDECREF(version);
+  Py_XDECREF(held);
+  Py_XDECREF(torch);
+  return same ? PyModule_Create(&kModule) : nullptr;
+}

@@ -15,7 +15,22 @@ import ctypes
 import torch
 
 from .binding import _f32, _i32, _i64, _lib, _vp
-from . import _torch_calls  # after the library, which it links to
+
+
+class _Missing:
+    """In place of the module where it cannot be loaded: any call says why."""
+
+    def __init__(self, error):
+        self._why = f"{error}; run `python -m fp32_gemm_amd.build`"
+
+    def __getattr__(self, name):
+        raise ImportError(f"{name}: {self._why}")
+
+
+try:
+    from . import _torch_calls  # after the library, which it links to
+except ImportError as error:
+    _torch_calls = _Missing(error)
 
 _SIGS = {
     "gemm_grouped": ([_i32, _i32, _i32, _i32, _vp, _i64, _i64, _i64, _f32, _vp, _i64, _vp, _i64, _i64,
