@@ -99,12 +99,11 @@ Plan plan(int form, int type, int out, int groups, long long M, long long N, lon
     else if (shape <= kDeep) n = std::ceil(n);
     // Long reductions of ragged groups: where all tiles are resident at once,
     // long ones share a unit to the end; one at a time, the longest first, they
-    // even out.  Over 13 sizes of 257 to 512 tiles whose groups' lengths are up
-    // to six apart, kMid takes 1.01 to 1.31 of kDeep's time in f32 (8000 rows
-    // over 8, 1024 x 1024: 170 us and 144; equal groups 134 and 136, .85 to
-    // 1.02).  16-bit types, whose slices are short beside a tile's ends, gain
-    // nothing: .86 to 1.29, half of them below 1 (the same size in bf16: 34.8
-    // and 34.2), and equal groups lose (30.3 and 35.2, .80 to .98).
+    // even out.  Over 13 sizes of 257 to 512 tiles, with lengths up to six times
+    // apart and with equal ones, kMid takes on average 1.17 and .95 of kDeep's
+    // time in f32 (8000 rows over 8, 1024 x 1024: 172 us and 144; equal groups
+    // 135 and 138), but 1.01 to 1.03 and .88 to .90 in bf16, whose slices are
+    // short beside a tile's ends (35.3 and 34.5; equal groups 30.5 and 35.1).
     if (form == kFormTN && type == kElemF32 && groups > 1 && shape == kMid && n == 2 && slices >= kLongSlices)
       n = 2.5;
     if (shape == kSmall && n > 1) n += 0.5;

@@ -16,9 +16,9 @@
 // 16 of those bytes.
 //
 // What bounds it: many rows, the matrix cores and the power they draw (bf16
-// 8192 x 8192 x 8192 with transposed weights 787-825 us, 1335-1400 TFLOP/s at
-// 1.5 GHz; int8 420 us, 2620 TOP/s); few rows, reading the weights (32 experts,
-// 16 rows, 2048 to 1024: 9.7 us, 5.3 TB/s); small products, a launch and the
+// 8192 x 8192 x 8192 with transposed weights 808 us, 1362 TFLOP/s at about
+// 1.5 GHz; int8 442 us, 2490 TOP/s); few rows, reading the weights (32 experts,
+// 16 rows, 2048 to 1024: 10.0 us, 5.2 TB/s); small products, a launch and the
 // latencies of the offsets, the first slice and the results (4 us).
 #pragma once
 

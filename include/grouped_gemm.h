@@ -19,7 +19,8 @@
  * only the outputs' windows are written; bytes between an operand's rows may be
  * read (never used), none before its first or past its last.  The library allocates
  * nothing, uses no workspace and keeps no pointer.  Outputs must not overlap
- * inputs.
+ * inputs: an operand counts from its first byte to its last, so column ranges of
+ * one buffer are refused too (SGEMM_ERR_OVERLAP).
  *
  * Asynchrony, thread safety, graph capture: each call enqueues one kernel on
  * `stream` (a hipStream_t; NULL = default stream) and nothing else; it may be
@@ -92,6 +93,7 @@ int quantize_rows(int32_t type, int64_t M, int64_t K, const void* X, int64_t ldx
 /* C[r,n] = (sum_k A[r,k] * B_e[n,k]) * (scale_a[r] * scale_b[e,n]) + bias[e,n]
  * for every row r of every group e.  A is M x K and B_e = B + e * stride_b is
  * N x K, both int8; sums are exact 32-bit integers, rounded to a float once.
+ * The two scales are multiplied first, as 32-bit floats.
  * scale_a has M entries, scale_b and bias (or NULL) groups x N, all tight.
  * out_type: C's.  K == 0 gives the bias.
  * -1 out_type  -2 groups < 1, or not 1 without offsets  -4 M  -5 N  -6 K
