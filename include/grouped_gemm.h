@@ -9,7 +9,7 @@
  * `offsets` is a DEVICE array of groups + 1 increasing int32 row numbers
  * between 0 and M, read by the kernels when they run, so a router's counts need
  * not come back to the host.  Groups may be empty; rows that no group owns are
- * left as they are.  Offsets out of that range or order give wrong results but
+ * left as they are.  Offsets out of that range or order give wrong results or none, but
  * no access outside the operands.  offsets == NULL means one group of all M
  * rows.
  *
