@@ -40,8 +40,11 @@ HIP_FLAGS = [
 
 VALU, MFMA32, MFMA16 = 0, 1, 2
 
-# The grouped and 8-bit products (include/grouped_gemm.h), a unit per type.
-RAGGED = ("ragged_api", "ragged_f32", "ragged_bf16", "ragged_f16", "ragged_i8")
+# The grouped, 8-bit and 4-bit products (include/grouped_gemm.h), a unit per type.
+RAGGED = ("ragged_api", "ragged_f32", "ragged_bf16", "ragged_f16", "ragged_i8", "ragged_mx4")
+
+# The norm and the layer of experts for few tokens (include/layer_ops.h).
+LAYERS = ("layer_api", "norm", "expert_layer")
 
 
 # Tuples whose kernel (in either variant) the compiler had to spill to
@@ -404,7 +407,7 @@ def _build_once(verbose, jobs):
     api = os.path.join(CSRC, "sgemm_api.hip")
     work = [(api, os.path.join(BUILD, "sgemm_api.o"), False),
             (os.path.join(CSRC, "ladder.hip"), os.path.join(BUILD, "ladder.o"), True)]
-    work += [(os.path.join(CSRC, n + ".hip"), os.path.join(BUILD, n + ".o"), True) for n in RAGGED]
+    work += [(os.path.join(CSRC, n + ".hip"), os.path.join(BUILD, n + ".o"), True) for n in RAGGED + LAYERS]
     work += [(s, s[:-4] + ".o", True) for s in t_srcs]
     resources = {}
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:

@@ -1,0 +1,516 @@
+// norm.hip -- the root-mean-square norm of rows, with a residual's addition and
+// an 8-bit output, and its gradient.
+//
+//   h = x + r,  s = (mean h^2 + eps)^(-1/2),  v = h w,  y = s v
+//   scale = s max|v| / 127,  code = nearest(127 v / max|v|)
+//   dx = s (g - n mean(g n)) + dh,  dw = sum over rows of dy n,  g = dy w, n = h s
+//
+// Sums of squares, s and the largest |v| are held in 64 bits, so that no row of
+// finite numbers overflows and codes are those of the exact quotients.
+#include "norm.hpp"
+
+#include "ragged_kernels.hpp"
+
+namespace fp32gemm {
+namespace {
+
+template <int ELEM>
+__device__ __forceinline__ float element(const char* p, long long i) {
+  if constexpr (ELEM == kElemF32) return reinterpret_cast<const float*>(p)[i];
+  else if constexpr (ELEM == kElemBF16) return static_cast<float>(reinterpret_cast<const __bf16*>(p)[i]);
+  else return static_cast<float>(reinterpret_cast<const _Float16*>(p)[i]);
+}
+template <int ELEM>
+__device__ __forceinline__ void set_element(char* p, long long i, float v) {
+  if constexpr (ELEM == kElemF32) reinterpret_cast<float*>(p)[i] = v;
+  else if constexpr (ELEM == kElemBF16) reinterpret_cast<__bf16*>(p)[i] = static_cast<__bf16>(v);
+  else reinterpret_cast<_Float16*>(p)[i] = static_cast<_Float16>(v);
+}
+
+// Sixteen bytes of a row: PER elements from any byte on.
+template <int ELEM>
+struct Piece {
+  static constexpr int PER = 16 / elem_size(ELEM);
+  ri4 raw;
+  __device__ __forceinline__ void load(const char* p, long long piece) { __builtin_memcpy(&raw, p + piece * 16, 16); }
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (ELEM == kElemF32) return __builtin_bit_cast(rf4, raw)[i];
+    else if constexpr (ELEM == kElemBF16) return static_cast<float>(__builtin_bit_cast(rb8, raw)[i]);
+    else return static_cast<float>(__builtin_bit_cast(rh8, raw)[i]);
+  }
+  static __device__ __forceinline__ void store(char* p, long long piece, const float (&v)[PER]) {
+    ri4 w;
+    if constexpr (ELEM == kElemF32) {
+      w = __builtin_bit_cast(ri4, rf4{v[0], v[1], v[2], v[3]});
+    } else if constexpr (ELEM == kElemBF16) {
+      rb8 b;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) b[i] = static_cast<__bf16>(v[i]);
+      w = __builtin_bit_cast(ri4, b);
+    } else {
+      rh8 b;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) b[i] = static_cast<_Float16>(v[i]);
+      w = __builtin_bit_cast(ri4, b);
+    }
+    __builtin_memcpy(p + piece * 16, &w, 16);
+  }
+};
+
+// PER weights, of the rows' type or (W32) 32-bit floats; ones where there are none.
+template <int ELEM, bool W32>
+struct Weights {
+  static constexpr int PER = Piece<ELEM>::PER, WORDS = W32 ? PER / 4 : 1;
+  static constexpr int WELEM = W32 ? kElemF32 : ELEM;
+  Piece<WELEM> part[WORDS];
+  __device__ __forceinline__ void load(const char* w, long long piece) {
+    if (w == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) part[i].load(w, piece * WORDS + i);
+  }
+  __device__ __forceinline__ float at(const char* w, int i) const {
+    if (w == nullptr) return 1.0f;
+    if constexpr (W32) return part[i / 4][i % 4];
+    else return part[0][i];
+  }
+  static __device__ __forceinline__ float one(const char* w, long long i) {
+    return w == nullptr ? 1.0f : element<WELEM>(w, i);
+  }
+};
+
+// A value of another lane, by the patterns of a sum over all lanes below.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double from_lane(double v, double none) {
+  const ru2 w = __builtin_bit_cast(ru2, v), z = __builtin_bit_cast(ru2, none);
+  return __builtin_bit_cast(double, ru2{static_cast<unsigned>(__builtin_amdgcn_update_dpp(z[0], w[0], CTRL, ROWS, 0xF, false)),
+                                        static_cast<unsigned>(__builtin_amdgcn_update_dpp(z[1], w[1], CTRL, ROWS, 0xF, false))});
+}
+struct Add {
+  static constexpr double kNone = 0.0;
+  static __device__ __forceinline__ double of(double a, double b) { return a + b; }
+};
+struct Larger {
+  static constexpr double kNone = 0.0;  // magnitudes
+  static __device__ __forceinline__ double of(double a, double b) { return __builtin_fmax(a, b); }
+};
+// Over the wave, in lane 63.
+template <class F>
+__device__ __forceinline__ double over_wave(double v) {
+  v = F::of(v, from_lane<0x111, 0xF>(v, F::kNone));
+  v = F::of(v, from_lane<0x112, 0xF>(v, F::kNone));
+  v = F::of(v, from_lane<0x114, 0xF>(v, F::kNone));
+  v = F::of(v, from_lane<0x118, 0xF>(v, F::kNone));
+  v = F::of(v, from_lane<0x142, 0xA>(v, F::kNone));
+  v = F::of(v, from_lane<0x143, 0xC>(v, F::kNone));
+  return v;
+}
+__device__ __forceinline__ double last_lane(double v) {
+  const ru2 w = __builtin_bit_cast(ru2, v);
+  return __builtin_bit_cast(double, ru2{static_cast<unsigned>(__builtin_amdgcn_readlane(w[0], 63)),
+                                        static_cast<unsigned>(__builtin_amdgcn_readlane(w[1], 63))});
+}
+// Both over the THREADS threads of a row, known to all of them.  `room` holds two
+// values a wave; calls that follow one another take rooms in turn.
+template <class F, class G, int THREADS>
+__device__ __forceinline__ void over_row(double& a, double& b, double (*room)[2]) {
+  a = over_wave<F>(a);
+  b = over_wave<G>(b);
+  if constexpr (THREADS == 64) {
+    a = last_lane(a);
+    b = last_lane(b);
+  } else {
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 63) {
+      room[wave][0] = a;
+      room[wave][1] = b;
+    }
+    __syncthreads();
+    a = room[0][0];
+    b = room[0][1];
+#pragma unroll
+    for (int i = 1; i < THREADS / 64; ++i) {
+      a = F::of(a, room[i][0]);
+      b = G::of(b, room[i][1]);
+    }
+  }
+}
+
+// 1 / sqrt(m): the instruction's estimate and a step of Newton's method, which
+// squares its error; exact limits at 0 and infinity.
+__device__ __forceinline__ double inverse_root(double m) {
+  const double y = __builtin_amdgcn_rsq(m);
+  return m == 0.0 || m == __builtin_inf() ? y : y * __builtin_fma(-0.5 * m * y, y, 1.5);
+}
+
+// A code decided in 32 bits is off by at most 127 * 6 * 2^-24 before it is
+// rounded (h, v, the largest |v|, its inverse and the product round once each), so
+// values that near a tie, and rows whose inverse might leave the range, are
+// divided in 64 bits.
+constexpr float kNearTie = 0x1p-13f;
+
+constexpr int kNormBlocks = 1 << 23;  // workgroups in x; more rows go on in y
+
+// One row by THREADS threads of 256, KEEP pieces a thread in registers as they
+// came; longer rows are read again.  H may be x or r itself: a thread has read
+// what it overwrites, and where rows are read twice, H is written the second time.
+template <int ELEM, bool W32, int THREADS, int KEEP, bool CODES>
+__global__ __launch_bounds__(256) void rms_norm_kernel(const NormArgs p) {
+#ifdef __HIP_DEVICE_COMPILE__
+  using P = Piece<ELEM>;
+  using W = Weights<ELEM, W32>;
+  constexpr int ES = elem_size(ELEM), PER = P::PER;
+  __shared__ double room[4][2];
+  const int in = threadIdx.x % THREADS;
+  const long long block = static_cast<long long>(blockIdx.y) * kNormBlocks + blockIdx.x;
+  const long long row = block * (256 / THREADS) + threadIdx.x / THREADS;
+  const bool live = row < p.M;  // uniform in a wave
+  const char* const x = p.x + (live ? row : 0) * p.ldx * ES;
+  const char* const r = p.r == nullptr ? nullptr : p.r + (live ? row : 0) * p.ldr * ES;
+  const int pieces = live ? p.K / PER : 0, rest = live ? p.K % PER : 0;
+  const long long last = static_cast<long long>(pieces) * PER + in;
+  const bool one = in < rest;
+
+  P kx[KEEP], kr[KEEP];
+#pragma unroll
+  for (int j = 0; j < KEEP; ++j) {
+    const int c = in + j * THREADS;
+    kx[j].raw = kr[j].raw = ri4{};
+    if (c < pieces) {
+      kx[j].load(x, c);
+      if (r) kr[j].load(r, c);
+    }
+  }
+  const float x1 = one ? element<ELEM>(x, last) : 0.0f, r1 = one && r ? element<ELEM>(r, last) : 0.0f;
+  double sum = 0, top = 0, bad = 0;
+  auto take = [&](float a, float b, float w) {
+    const double h = static_cast<double>(a) + static_cast<double>(b);
+    sum = __builtin_fma(h, h, sum);
+    if constexpr (CODES) {
+      const double v = h * static_cast<double>(w);
+      top = __builtin_fmax(top, __builtin_fabs(v));
+      bad = __builtin_fma(v, 0.0, bad);  // NaN once a value is not finite
+    }
+  };
+  auto take_piece = [&](const P& a, const P& b, int c) {
+    W w;
+    if constexpr (CODES) w.load(p.w, c);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) take(a[i], b[i], CODES ? w.at(p.w, i) : 1.0f);
+  };
+#pragma unroll
+  for (int j = 0; j < KEEP; ++j) {
+    const int c = in + j * THREADS;
+    if (c < pieces) take_piece(kx[j], kr[j], c);
+  }
+  if (one) take(x1, r1, CODES ? W::one(p.w, last) : 1.0f);
+  for (int c = in + KEEP * THREADS; c < pieces; c += THREADS) {
+    P a, b;
+    a.load(x, c);
+    b.raw = ri4{};
+    if (r) b.load(r, c);
+    take_piece(a, b, c);
+  }
+  if constexpr (CODES)
+    if (bad != 0.0) top = __builtin_inf();
+  over_row<Add, Larger, THREADS>(sum, top, room);
+  const double s = inverse_root(__builtin_fma(sum, p.inv_k, static_cast<double>(p.eps)));
+  // s in 32 bits, with a power of two of its own where it would leave their range.
+  const float before = s < 0x1p-100 ? 0x1p-64f : s > 0x1p100 ? 0x1p64f : 1.0f;
+  const float s32 = static_cast<float>(s < 0x1p-100 ? s * 0x1p64 : s > 0x1p100 ? s * 0x1p-64 : s);
+  const bool usable = top > 0.0 && top < __builtin_inf();
+  const bool in_64 = !(top > 0x1p-100 && top < 0x1p100);
+  const float inv = in_64 ? 0.0f : 127.0f / static_cast<float>(top);
+  if (!live) return;
+  if constexpr (CODES)
+    if (in == 0) p.scale[row] = top == __builtin_inf() ? __builtin_nanf("") : static_cast<float>(top / 127.0 * s);
+
+  char* const h = p.h ? p.h + row * p.ldh * ES : nullptr;
+  char* const y = p.y ? p.y + row * p.ldy * (p.out32 ? 4 : ES) : nullptr;
+  signed char* const q = CODES ? p.q + row * p.ldq : nullptr;
+  auto code64 = [&](float a, float b, float w) {
+    const double v = (static_cast<double>(a) + static_cast<double>(b)) * static_cast<double>(w);
+    return usable ? static_cast<int>(__builtin_rint(v * 127.0 / top)) : 0;
+  };
+  auto write = [&](const P& a, const P& b, int c) {
+    W w;
+    w.load(p.w, c);
+    float hv[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) hv[i] = a[i] + b[i];
+    if (h) P::store(h, c, hv);
+    if constexpr (CODES) {
+      int code[PER];
+      bool near = in_64;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const float t = hv[i] * w.at(p.w, i) * inv, n = __builtin_rintf(t);
+        near |= __builtin_fabsf(__builtin_fabsf(t - n) - 0.5f) < kNearTie;
+        code[i] = static_cast<int>(n);
+      }
+      if (near)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) code[i] = code64(a[i], b[i], w.at(p.w, i));
+      unsigned o[PER / 4];
+#pragma unroll
+      for (int i = 0; i < PER / 4; ++i)
+        o[i] = (code[4 * i] & 255u) | (code[4 * i + 1] & 255u) << 8 | (code[4 * i + 2] & 255u) << 16 |
+               static_cast<unsigned>(code[4 * i + 3]) << 24;
+      __builtin_memcpy(q + static_cast<long long>(c) * PER, o, PER);
+    }
+    if (y) {
+      float v[PER];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[i] = hv[i] * before * s32 * w.at(p.w, i);
+      if (ELEM != kElemF32 && p.out32) __builtin_memcpy(y + static_cast<long long>(c) * PER * 4, v, PER * 4);
+      else P::store(y, c, v);
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < KEEP; ++j) {
+    const int c = in + j * THREADS;
+    if (c < pieces) write(kx[j], kr[j], c);
+  }
+  if (one) {
+    const float hv = x1 + r1, w = W::one(p.w, last);
+    if (h) set_element<ELEM>(h, last, hv);
+    if constexpr (CODES) q[last] = static_cast<signed char>(code64(x1, r1, w));
+    if (y) {
+      const float v = hv * before * s32 * w;
+      if (ELEM != kElemF32 && p.out32) reinterpret_cast<float*>(y)[last] = v;
+      else set_element<ELEM>(y, last, v);
+    }
+  }
+  for (int c = in + KEEP * THREADS; c < pieces; c += THREADS) {
+    P a, b;
+    a.load(x, c);
+    b.raw = ri4{};
+    if (r) b.load(r, c);
+    write(a, b, c);
+  }
+#endif
+}
+
+// The gradient: a team of THREADS threads takes every teams-th row, with its sums
+// for dw in registers, P pieces a thread (0: any length, the sums in memory), and
+// leaves them as a row of `partial`.
+template <int ELEM, bool W32, int THREADS, int PIECES>
+__global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_grad_kernel(const NormGradArgs p) {
+#ifdef __HIP_DEVICE_COMPILE__
+  using P = Piece<ELEM>;
+  using W = Weights<ELEM, W32>;
+  constexpr int ES = elem_size(ELEM), PER = P::PER, HELD = PIECES ? PIECES : 1;
+  constexpr int TEAMS = THREADS < 256 ? 256 / THREADS : 1;  // of a workgroup
+  __shared__ double room[2][THREADS / 64][2];
+  const int in = threadIdx.x % THREADS;
+  const int team = blockIdx.x * TEAMS + threadIdx.x / THREADS;
+  if (team >= p.teams) return;  // uniform in a wave; teams of several waves are whole workgroups
+  const int pieces = p.K / PER, rest = p.K % PER;
+  const long long last = static_cast<long long>(pieces) * PER + in;
+  const bool one = in < rest;
+  const float w1 = one ? W::one(p.w, last) : 0.0f;
+  float* const part = p.partial ? p.partial + static_cast<long long>(team) * p.K : nullptr;
+  float dw[HELD][PER] = {}, dw1 = 0.0f;
+  W w[HELD];
+  if constexpr (PIECES)
+#pragma unroll
+    for (int j = 0; j < HELD; ++j)
+      if (in + j * THREADS < pieces) w[j].load(p.w, in + j * THREADS);
+  int turn = 0;
+  for (int row = team; row < p.M; row += p.teams, turn ^= 1) {
+    const char* const h = p.h + row * p.ldh * ES;
+    const char* const dy = p.dy + row * p.lddy * ES;
+    const char* const dh = p.dh ? p.dh + row * p.lddh * ES : nullptr;
+    char* const dx = p.dx + row * p.lddx * ES;
+    double square = 0, dot = 0;
+    auto take = [&](float a, float b, float wv) {
+      const double d = a;
+      square = __builtin_fma(d, d, square);
+      dot = __builtin_fma(d, static_cast<double>(b * wv), dot);
+    };
+    P kh[HELD], kd[HELD], kr[HELD];
+    if constexpr (PIECES) {
+#pragma unroll
+      for (int j = 0; j < HELD; ++j) {
+        const int c = in + j * THREADS;
+        kh[j].raw = kd[j].raw = kr[j].raw = ri4{};
+        if (c < pieces) {
+          kh[j].load(h, c);
+          kd[j].load(dy, c);
+          if (dh) kr[j].load(dh, c);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < HELD; ++j)
+        if (in + j * THREADS < pieces)
+#pragma unroll
+          for (int i = 0; i < PER; ++i) take(kh[j][i], kd[j][i], w[j].at(p.w, i));
+    } else {
+      for (int c = in; c < pieces; c += THREADS) {
+        P a, b;
+        a.load(h, c);
+        b.load(dy, c);
+        w[0].load(p.w, c);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) take(a[i], b[i], w[0].at(p.w, i));
+      }
+    }
+    const float h1 = one ? element<ELEM>(h, last) : 0.0f, d1 = one ? element<ELEM>(dy, last) : 0.0f;
+    const float r1 = one && dh ? element<ELEM>(dh, last) : 0.0f;
+    if (one) take(h1, d1, w1);
+    over_row<Add, Add, THREADS>(square, dot, room[turn]);
+    const double s64 = inverse_root(__builtin_fma(square, p.inv_k, static_cast<double>(p.eps)));
+    const float s = static_cast<float>(s64), mean = static_cast<float>(dot * p.inv_k * s64);
+    auto grad = [&](float a, float b, float r, float wv, float& sums) {
+      const float n = a * s;
+      sums = __builtin_fmaf(b, n, sums);
+      return __builtin_fmaf(s, __builtin_fmaf(-n, mean, b * wv), r);
+    };
+    auto piece = [&](const P& a, const P& b, const P& r, const W& wv, int c, float (&sums)[PER]) {
+      float v[PER];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[i] = grad(a[i], b[i], r[i], wv.at(p.w, i), sums[i]);
+      P::store(dx, c, v);
+    };
+    if constexpr (PIECES) {
+#pragma unroll
+      for (int j = 0; j < HELD; ++j)
+        if (in + j * THREADS < pieces) piece(kh[j], kd[j], kr[j], w[j], in + j * THREADS, dw[j]);
+    } else {
+      for (int c = in; c < pieces; c += THREADS) {
+        P a, b, r;
+        a.load(h, c);
+        b.load(dy, c);
+        r.raw = ri4{};
+        if (dh) r.load(dh, c);
+        w[0].load(p.w, c);
+        float sums[PER] = {};
+        float* const at = part ? part + static_cast<long long>(c) * PER : nullptr;
+        if (at && row != team) __builtin_memcpy(sums, at, PER * 4);
+        piece(a, b, r, w[0], c, sums);
+        if (at) __builtin_memcpy(at, sums, PER * 4);
+      }
+    }
+    if (one) set_element<ELEM>(dx, last, grad(h1, d1, r1, w1, dw1));
+  }
+  if (part) {
+    if constexpr (PIECES)
+#pragma unroll
+      for (int j = 0; j < HELD; ++j) {
+        const int c = in + j * THREADS;
+        if (c < pieces) __builtin_memcpy(part + static_cast<long long>(c) * PER, dw[j], PER * 4);
+      }
+    if (one) part[last] = dw1;
+  }
+#endif
+}
+
+// dw: the teams' sums, a column by four threads that take every 4th team, in a
+// fixed order.
+constexpr int kSumColumns = 64, kSumGroups = 16;
+template <int OUT>
+__global__ __launch_bounds__(kSumColumns* kSumGroups) void sum_partial_kernel(const float* partial, int teams, int K,
+                                                                             char* dw) {
+#ifdef __HIP_DEVICE_COMPILE__
+  __shared__ float sums[kSumGroups][kSumColumns];
+  const int c = threadIdx.x % kSumColumns, g = threadIdx.x / kSumColumns;
+  const long long col = static_cast<long long>(blockIdx.x) * kSumColumns + c;
+  float sum = 0.0f;
+  if (col < K)
+#pragma unroll 8
+    for (int t = g; t < teams; t += kSumGroups) sum += partial[static_cast<long long>(t) * K + col];
+  sums[g][c] = sum;
+  __syncthreads();
+  if (g == 0 && col < K) {
+#pragma unroll
+    for (int i = 1; i < kSumGroups; ++i) sum += sums[i][c];
+    set_element<OUT>(dw, col, sum);
+  }
+#endif
+}
+
+template <int ELEM, bool W32, int THREADS, int KEEP>
+const void* norm_kernel(bool codes) {
+  return codes ? reinterpret_cast<const void*>(&rms_norm_kernel<ELEM, W32, THREADS, KEEP, true>)
+               : reinterpret_cast<const void*>(&rms_norm_kernel<ELEM, W32, THREADS, KEEP, false>);
+}
+
+template <int ELEM, bool W32>
+hipError_t launch_norm(const NormArgs& args, hipStream_t s) {
+  // A wave takes rows of up to two pieces a lane, and of up to eight where there
+  // are rows enough for all waves; longer ones go to four waves.
+  const int pieces = args.K / Piece<ELEM>::PER;
+  const bool wave = pieces <= 128 || (pieces <= 512 && args.M >= 4096), codes = args.scale != nullptr;
+  const int each = wave ? (pieces + 63) / 64 : (pieces + 255) / 256;
+  const void* const kernel = wave ? (each <= 1   ? norm_kernel<ELEM, W32, 64, 1>(codes)
+                                     : each <= 2 ? norm_kernel<ELEM, W32, 64, 2>(codes)
+                                     : each <= 4 ? norm_kernel<ELEM, W32, 64, 4>(codes)
+                                                 : norm_kernel<ELEM, W32, 64, 8>(codes))
+                                  : (each <= 1   ? norm_kernel<ELEM, W32, 256, 1>(codes)
+                                     : each <= 2 ? norm_kernel<ELEM, W32, 256, 2>(codes)
+                                     : each <= 4 ? norm_kernel<ELEM, W32, 256, 4>(codes)
+                                                 : norm_kernel<ELEM, W32, 256, 8>(codes));
+  const unsigned blocks = wave ? (static_cast<unsigned>(args.M) + 3) / 4 : static_cast<unsigned>(args.M);
+  const dim3 grid(blocks < kNormBlocks ? blocks : kNormBlocks, (blocks + kNormBlocks - 1) / kNormBlocks);
+  NormArgs a = args;
+  void* values[] = {&a};
+  return hipLaunchKernel(kernel, grid, dim3(256), values, 0, s);
+}
+
+template <int ELEM, bool W32>
+hipError_t launch_grad(const NormGradArgs& args, hipStream_t s) {
+  const int pieces = args.K / Piece<ELEM>::PER;
+  const void* kernel;
+  int threads;
+  auto pick = [&](int t, const void* k) {
+    threads = t;
+    kernel = k;
+  };
+  if (pieces <= 64) pick(64, reinterpret_cast<const void*>(&rms_norm_grad_kernel<ELEM, W32, 64, 1>));
+  else if (pieces <= 128) pick(64, reinterpret_cast<const void*>(&rms_norm_grad_kernel<ELEM, W32, 64, 2>));
+  else if (pieces <= 256) pick(256, reinterpret_cast<const void*>(&rms_norm_grad_kernel<ELEM, W32, 256, 1>));
+  else if (pieces <= 512) pick(256, reinterpret_cast<const void*>(&rms_norm_grad_kernel<ELEM, W32, 256, 2>));
+  else if (pieces <= 1024) pick(256, reinterpret_cast<const void*>(&rms_norm_grad_kernel<ELEM, W32, 256, 4>));
+  else if (pieces <= 2048) pick(1024, reinterpret_cast<const void*>(&rms_norm_grad_kernel<ELEM, W32, 1024, 2>));
+  else pick(1024, reinterpret_cast<const void*>(&rms_norm_grad_kernel<ELEM, W32, 1024, 0>));
+  NormGradArgs a = args;
+  void* values[] = {&a};
+  const unsigned each = threads < 256 ? 256 / threads : 1;
+  return hipLaunchKernel(kernel, dim3((static_cast<unsigned>(args.teams) + each - 1) / each),
+                         dim3(threads < 256 ? 256 : threads), values, 0, s);
+}
+
+}  // namespace
+
+int norm_teams(long long M) {
+  // Every team writes a row of sums: one for at least 16 rows, so that they are
+  // few beside the rows, but as many as there are rows until the card is full.
+  const long long most = M / 16;
+  return static_cast<int>(M <= 512 ? M : most < 512 ? 512 : most < 1024 ? most : 1024);
+}
+
+hipError_t rms_norm_launch(int type, bool w32, const NormArgs& a, hipStream_t s) {
+  if (type == kElemF32) return launch_norm<kElemF32, false>(a, s);
+  if (type == kElemBF16) return w32 ? launch_norm<kElemBF16, true>(a, s) : launch_norm<kElemBF16, false>(a, s);
+  return w32 ? launch_norm<kElemF16, true>(a, s) : launch_norm<kElemF16, false>(a, s);
+}
+
+hipError_t rms_norm_grad_launch(int type, bool w32, int dw_type, char* dw, const NormGradArgs& a, hipStream_t s) {
+  if (a.M > 0) {
+    const hipError_t err =
+        type == kElemF32    ? launch_grad<kElemF32, false>(a, s)
+        : type == kElemBF16 ? (w32 ? launch_grad<kElemBF16, true>(a, s) : launch_grad<kElemBF16, false>(a, s))
+                            : (w32 ? launch_grad<kElemF16, true>(a, s) : launch_grad<kElemF16, false>(a, s));
+    if (err != hipSuccess) return err;
+  }
+  if (dw == nullptr) return hipSuccess;
+  const float* partial = a.partial;
+  int teams = a.M > 0 ? a.teams : 0, K = a.K;
+  void* values[] = {&partial, &teams, &K, &dw};
+  const void* const kernel = dw_type == kElemF32    ? reinterpret_cast<const void*>(&sum_partial_kernel<kElemF32>)
+                             : dw_type == kElemBF16 ? reinterpret_cast<const void*>(&sum_partial_kernel<kElemBF16>)
+                                                    : reinterpret_cast<const void*>(&sum_partial_kernel<kElemF16>);
+  return hipLaunchKernel(kernel, dim3(static_cast<unsigned>((static_cast<long long>(K) + kSumColumns - 1) / kSumColumns)),
+                         dim3(kSumColumns * kSumGroups), values, 0, s);
+}
+
+}  // namespace fp32gemm

@@ -10,11 +10,14 @@
 #include "../../include/grouped_gemm.h"
 #include "ragged_host_wave.hpp"
 #include "ragged_kernels.hpp"
+#include "windows.hpp"
 
 namespace fp32gemm {
 
 hipError_t quantize_launch(int type, const char* x, long long ldx, signed char* q, long long ldq,
                            float* scale, int M, int K, hipStream_t s);
+hipError_t quantize_mx4_launch(int type, const char* x, long long ldx, unsigned char* q, long long ldq,
+                               unsigned char* scale, int M, int K, hipStream_t s);
 void set_last_hip_error(hipError_t e);  // sgemm_api.hip
 
 namespace {
@@ -22,15 +25,6 @@ namespace {
 constexpr long long kMaxDim = 1LL << 30, kMaxStride = 1LL << 40, kMaxGroups = 1 << 16;
 constexpr double kMaxThreads = 4294967295.0;  // of a launch: HIP holds workgroups x threads in 32 bits
 constexpr long long kMaxIntegerK = 131071;  // 131071 * 128 * 128 < 2^31
-
-// Bytes of a rows x cols window, and whether two windows share any.
-long long extent(long long rows, long long cols, long long ld, int es) {
-  return rows > 0 && cols > 0 ? ((rows - 1) * ld + cols) * es : 0;
-}
-bool overlap(const void* a, long long an, const void* b, long long bn) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return an > 0 && bn > 0 && x < y + static_cast<uintptr_t>(bn) && y < x + static_cast<uintptr_t>(an);
-}
 
 struct Plan {
   int shape;
@@ -42,7 +36,7 @@ struct Plan {
 // What a tile costs, in microseconds as measured: a slice of 128 bytes of the
 // reduction on a busy compute unit and on one that holds no other tile, and a
 // tile's start and end with results of 2 and of 4 bytes.  32-bit floats take
-// four times the matrix instructions a slice.
+// four times the matrix instructions a slice; 4-bit codes as many as 8-bit ones.
 struct TileCost { double busy, alone, ends2, ends4; };
 constexpr TileCost kCost16[kShapes] = {{1.4, 1.4, 7.2, 8.5}, {.50, .64, 2.0, 2.5}, {.54, .52, 2.3, 3},
                                        {.19, .28, .9, .9},    {.135, .2, .5, .5},   {.09, .11, .5, .5}};
@@ -151,6 +145,7 @@ int launch(int type, int form, const RaggedArgs& a, long long M, long long N, lo
   const hipError_t err = type == kElemF32    ? ragged_f32(form, p.shape, args, p.grid, s)
                          : type == kElemBF16 ? ragged_bf16(form, p.shape, args, p.grid, s)
                          : type == kElemF16  ? ragged_f16(form, p.shape, args, p.grid, s)
+                         : type == kElemM4   ? ragged_m4(form, p.shape, args, p.grid, s)
                                              : ragged_i8(form, p.shape, args, p.grid, s);
   if (err != hipSuccess) {
     set_last_hip_error(err);
@@ -163,8 +158,8 @@ bool float_type(int t) { return t == GEMM_F32 || t == GEMM_BF16 || t == GEMM_F16
 long long at_least(long long n) { return n > 1 ? n : 1; }
 
 bool plan_arguments(int form, int type, int out_type, int groups, long long M, long long N, long long K) {
-  return form >= kFormNT && form <= kFormTN && type >= kElemF32 && type <= kElemI8 &&
-         (type != kElemI8 || form == kFormNT) && float_type(out_type) && groups >= 1 && groups <= kMaxGroups &&
+  const bool typed = float_type(type) || ((type == kElemI8 || type == kElemM4) && form == kFormNT);
+  return form >= kFormNT && form <= kFormTN && typed && float_type(out_type) && groups >= 1 && groups <= kMaxGroups &&
          M >= 0 && N >= 0 && K >= 0 && M <= kMaxDim && N <= kMaxDim && K <= kMaxDim;
 }
 
@@ -342,6 +337,83 @@ int igemm(int32_t out_type, int32_t groups, const int32_t* offsets, int64_t M, i
   a.K = static_cast<int>(K);
   a.out = out_type;
   return launch(kElemI8, kFormNT, a, M, N, K, stream);
+}
+
+int quantize_mx4(int32_t type, int64_t M, int64_t K, const void* X, int64_t ldx, uint8_t* Q, int64_t ldq,
+                 uint8_t* scale, void* stream) {
+  if (!float_type(type)) return -1;
+  if (M < 0) return -2;
+  if (K < 0) return -3;
+  if (X == nullptr && M > 0 && K > 0) return -4;
+  if (ldx < at_least(K)) return -5;
+  if (Q == nullptr && M > 0 && K > 0) return -6;
+  if (ldq < at_least((K + 1) / 2)) return -7;
+  if (scale == nullptr && M > 0 && K > 0) return -8;
+  if (M > kMaxDim || K > kMaxDim || ldx > kMaxDim || ldq > kMaxDim) return SGEMM_ERR_UNSUPPORTED;
+  const long long x = extent(M, K, ldx, elem_size(type)), q = extent(M, (K + 1) / 2, ldq, 1);
+  const long long blocks = M * ((K + 31) / 32);
+  if (overlap(Q, q, X, x) || overlap(scale, blocks, X, x) || overlap(scale, blocks, Q, q))
+    return SGEMM_ERR_OVERLAP;
+  if (M == 0 || K == 0) return SGEMM_OK;
+  const int rc = sgemm_device_check();
+  if (rc != SGEMM_OK) return rc;
+  const hipError_t err = quantize_mx4_launch(type, static_cast<const char*>(X), ldx, Q, ldq, scale,
+                                             static_cast<int>(M), static_cast<int>(K),
+                                             static_cast<hipStream_t>(stream));
+  if (err != hipSuccess) {
+    set_last_hip_error(err);
+    return SGEMM_ERR_LAUNCH;
+  }
+  return SGEMM_OK;
+}
+
+int gemm_mx4(int32_t out_type, int32_t groups, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
+             const uint8_t* A, int64_t lda, const uint8_t* scale_a, const uint8_t* B, int64_t ldb,
+             int64_t stride_b, const uint8_t* scale_b, const float* bias, void* C, int64_t ldc, void* stream) {
+  if (!float_type(out_type)) return -1;
+  if (groups < 1 || (offsets == nullptr && groups != 1)) return -2;
+  if (M < 0) return -4;
+  if (N < 0) return -5;
+  if (K < 0) return -6;
+  if (A == nullptr && M > 0 && K > 0) return -7;
+  const long long bytes = (K + 1) / 2, blocks = (K + 31) / 32;  // of a row
+  if (lda < at_least(bytes)) return -8;
+  if (scale_a == nullptr && M > 0 && K > 0) return -9;
+  if (B == nullptr && N > 0 && K > 0) return -10;
+  if (ldb < at_least(bytes)) return -11;
+  if (stride_b < 0) return -12;
+  if (scale_b == nullptr && N > 0 && K > 0) return -13;
+  if (C == nullptr && M > 0 && N > 0) return -15;
+  if (ldc < at_least(N)) return -16;
+  if (M > kMaxDim || N > kMaxDim || K > kMaxDim || lda >= kRaggedMaxLd || ldb >= kRaggedMaxLd ||
+      ldc >= kRaggedMaxLd || stride_b > kMaxStride || groups > kMaxGroups)
+    return SGEMM_ERR_UNSUPPORTED;
+  const long long c = extent(M, N, ldc, elem_size(out_type)), b = extent(N, bytes, ldb, 1);
+  if (overlap(C, c, A, extent(M, bytes, lda, 1)) || overlap(C, c, B, b ? (groups - 1) * stride_b + b : 0) ||
+      overlap(C, c, scale_a, M * blocks) || overlap(C, c, scale_b, groups * N * blocks) ||
+      (bias && overlap(C, c, bias, 4LL * groups * N)) ||
+      (offsets && overlap(C, c, offsets, 4LL * (groups + 1))))
+    return SGEMM_ERR_OVERLAP;
+  if (M == 0 || N == 0) return SGEMM_OK;
+  RaggedArgs a{};
+  a.A = reinterpret_cast<const char*>(A);
+  a.B = reinterpret_cast<const char*>(B);
+  a.C = static_cast<char*>(C);
+  a.offsets = offsets;
+  a.block_a = scale_a;
+  a.block_b = scale_b;
+  a.bias = bias;
+  a.lda = lda;
+  a.ldb = ldb;
+  a.ldc = ldc;
+  a.stride_b = stride_b;
+  a.groups = groups;
+  a.rows = static_cast<int>(M);
+  a.M = static_cast<int>(M);
+  a.N = static_cast<int>(N);
+  a.K = static_cast<int>(bytes);
+  a.out = out_type;
+  return launch(kElemM4, kFormNT, a, M, N, bytes, stream);
 }
 
 int64_t gemm_grouped_plan(int32_t form, int32_t type, int32_t out_type, int32_t groups, int64_t M,

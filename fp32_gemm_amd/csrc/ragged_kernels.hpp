@@ -31,10 +31,11 @@
 
 namespace fp32gemm {
 
-enum Elem { kElemF32 = 0, kElemBF16 = 1, kElemF16 = 2, kElemI8 = 3 };
+// kElemM4: two 4-bit codes a byte, which is its element here, and a scale for every 16 bytes of a row.
+enum Elem { kElemF32 = 0, kElemBF16 = 1, kElemF16 = 2, kElemI8 = 3, kElemM4 = 5 };
 enum Form { kFormNT = 0, kFormNN = 1, kFormTN = 2 };
 
-constexpr int elem_size(int t) { return t == kElemF32 ? 4 : t == kElemI8 ? 1 : 2; }
+constexpr int elem_size(int t) { return t == kElemF32 ? 4 : t == kElemI8 || t == kElemM4 ? 1 : 2; }
 
 struct RaggedArgs {
   const char* A;
@@ -43,7 +44,9 @@ struct RaggedArgs {
   const int* offsets;     // groups + 1 row numbers; null: one group of all rows
   const float* scale_a;   // 8-bit products: a scale per row,
   const float* scale_b;   // a scale per group and column,
-  const float* bias;      // and a bias per group and column, or null
+  const float* bias;      // and a bias per group and column, or null (4-bit products too)
+  const unsigned char* block_a;  // 4-bit products: a power of two for every 16 bytes of a row,
+  const unsigned char* block_b;  // rows (and groups of rows) without gaps
   long long lda, ldb;     // bytes
   long long ldc;          // elements
   long long stride_b;     // bytes between the groups of B
@@ -82,6 +85,7 @@ typedef int ri4 __attribute__((ext_vector_type(4)));
 typedef int ri2 __attribute__((ext_vector_type(2)));
 typedef unsigned ru4 __attribute__((ext_vector_type(4)));
 typedef unsigned ru2 __attribute__((ext_vector_type(2)));
+typedef int ri8 __attribute__((ext_vector_type(8)));
 typedef int ri16 __attribute__((ext_vector_type(16)));
 typedef short rs4 __attribute__((ext_vector_type(4)));
 typedef __bf16 rb8 __attribute__((ext_vector_type(8)));
@@ -104,6 +108,7 @@ template <> struct RaggedAcc<kElemI8, 32> { using type = ri16; };
 template <> struct RaggedAcc<kElemF32, 16> { using type = rf4; };
 template <> struct RaggedAcc<kElemBF16, 16> { using type = rf4; };
 template <> struct RaggedAcc<kElemF16, 16> { using type = rf4; };
+template <> struct RaggedAcc<kElemM4, 16> { using type = rf4; };
 template <> struct RaggedAcc<kElemI8, 16> { using type = ri4; };
 
 // acc += b * a on one block: 32 bytes of the reduction with 32 x 32 blocks, 64
@@ -132,6 +137,18 @@ __device__ __forceinline__ void ragged_mma(Acc& acc, const ri4& b, const ri4& a)
       else acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[j], y[j], acc, 0, 0, 0);
     }
   }
+}
+
+// The same for 4-bit codes: 64 or 128 of the reduction, a lane's 16 bytes one
+// block of 32 codes with a scale, byte SEL of the lane's word of them.
+template <int SEL, int MF, class Acc>
+__device__ __forceinline__ void ragged_mma_blocks(Acc& acc, const ri4& b, const ri4& a, int scale_b, int scale_a) {
+  constexpr int kFp4 = 4;
+  const ri8 x = {b[0], b[1], b[2], b[3], 0, 0, 0, 0}, y = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
+  if constexpr (MF == 32)
+    acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, acc, kFp4, kFp4, SEL, scale_b, SEL, scale_a);
+  else
+    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, kFp4, kFp4, SEL, scale_b, SEL, scale_a);
 }
 
 // ---------------------------------------------------------------------------
@@ -257,6 +274,72 @@ struct RaggedLoader {
   }
 };
 
+// The scales of a slice of 4-bit codes: 8 bytes of every row of A, then of B,
+// brought to LDS as they lie, 4 bytes a lane and 32 rows a load instruction,
+// which the waves that share the slice divide.  What is past the slice's last
+// block reads as 2^-127, and its codes as zero.
+template <class T>
+struct RaggedBlocks {
+  static constexpr int ROW = T::SL / 16;  // bytes of a row's scales
+  static constexpr int UNITS_A = (T::BM + 31) / 32, UNITS_B = (T::BN + 31) / 32;
+  static constexpr int NI = (UNITS_A + UNITS_B) / T::WAVES;  // load instructions a wave
+  static constexpr int AT_B = UNITS_A * 256, STAGE = (UNITS_A + UNITS_B) * 256;
+  static_assert((UNITS_A + UNITS_B) % T::WAVES == 0 && ROW == 8, "whole load instructions a wave");
+  const char* base[NI];  // of the next slice
+  int off[NI];           // this lane's bytes past it, or kRaggedMasked
+  int first;             // the wave's first load instruction
+
+  __device__ __forceinline__ void init(const unsigned char* a, const unsigned char* b, int row_bytes, int rows_a,
+                                       int rows_b, int wave, int lane) {
+    first = wave * NI;
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      const int u = first + j;
+      const bool of_a = u < UNITS_A;
+      const int row = (of_a ? u : u - UNITS_A) * 32 + lane / 2;
+      base[j] = reinterpret_cast<const char*>(of_a ? a : b);
+      off[j] = row < (of_a ? rows_a : rows_b) ? row * row_bytes + lane % 2 * 4 : kRaggedMasked;
+    }
+  }
+  __device__ __forceinline__ void skip(int bytes) {
+#pragma unroll
+    for (int j = 0; j < NI; ++j) base[j] += bytes;
+  }
+  __device__ __forceinline__ void send(rlds_t stage, bool more, int step) {
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ragged_rsrc(base[j], more ? kRaggedMasked : 0),
+                                               (__attribute__((address_space(3))) void*)(stage + (first + j) * 256), 4,
+                                               off[j], 0, 0, 0);
+    skip(step);
+  }
+  // Of the slice `ahead` bytes on, `left` scales of which exist, through registers.
+  __device__ __forceinline__ void fetch(int (&held)[NI], int ahead, int left, int lane) const {
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      const auto r = ragged_rsrc(base[j] + ahead, kRaggedMasked);
+      held[j] = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool there = lane % 2 * 4 + i < left && off[j] != kRaggedMasked;
+        held[j] |= (__builtin_amdgcn_raw_buffer_load_b8(r, there ? off[j] + i : kRaggedMasked, 0, 0) & 255) << (8 * i);
+      }
+    }
+  }
+  __device__ __forceinline__ void put(const int (&held)[NI], rlds_t stage, int lane) const {
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+      *(__attribute__((address_space(3))) int*)(stage + (first + j) * 256 + lane * 4) = held[j];
+  }
+  // A lane's scales of a slice of one operand's block of rows, a byte for each of its pieces.
+  static __device__ __forceinline__ int word(rlds_t stage, int at, int lane) {
+    constexpr int EACH = ROW * T::MF / 64;  // bytes a lane takes
+    const rlds_t p = stage + (at + lane % T::MF) * ROW + lane / T::MF * EACH;
+    if constexpr (EACH == 4) return *(__attribute__((address_space(3))) int*)p;
+    else return *(__attribute__((address_space(3))) unsigned short*)p;
+  }
+};
+
 // The transposing read.  The restricted pointer tells the compiler that the
 // loads to LDS in flight do not write what is read here, which the barrier's
 // explicit wait sees to; without it every read would wait for all of them
@@ -274,7 +357,11 @@ __device__ __forceinline__ ri4 ragged_frag(rlds_t stage, int at, int ks, int lan
   constexpr int GROUPS = 64 / MF;  // 16-byte pieces of the reduction a block takes
   if constexpr (ALONG) {
     const int row = at + lane % MF;
-    const int piece = (ks * GROUPS + lane / MF) ^ L::swizzle(lane % MF);
+    // The order of the reduction's pieces is free as long as both operands keep
+    // it.  4-bit codes: a lane's pieces of a slice follow one another, so that
+    // the scales of all of them are one word.
+    constexpr int KS = SL / 16 / GROUPS;
+    const int piece = (ELEM == kElemM4 ? lane / MF * KS + ks : ks * GROUPS + lane / MF) ^ L::swizzle(lane % MF);
     return *(__attribute__((address_space(3))) ri4*)(stage + row * SL + piece * 16);
   } else if constexpr (L::ES == 2) {
     // Sixteen lanes read 4 steps x 16 columns (lane s: step s / 4, columns
@@ -318,7 +405,12 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
   using Acc = typename RaggedAcc<ELEM, MF>::type;
   using LoadA = RaggedLoader<ELEM, T::BM, A_ALONG, SL, T::WAVES>;
   using LoadB = RaggedLoader<ELEM, T::BN, B_ALONG, SL, T::WAVES>;
-  __shared__ __attribute__((aligned(1024))) char lds[T::LDS];
+  constexpr bool M4 = ELEM == kElemM4, BIASED = ELEM == kElemI8 || M4;
+  using Blocks = std::conditional_t<M4, RaggedBlocks<std::conditional_t<M4, T, RaggedTile<64, 64, 2, 2, 1, 2, 128, 32, 2>>>,
+                                    RaggedBlocks<RaggedTile<64, 64, 2, 2, 1, 2, 128, 32, 2>>>;
+  constexpr int NIS = M4 ? Blocks::NI : 0;  // load instructions of a slice's scales
+  constexpr int RING = T::RING + (M4 ? Blocks::STAGE * S * T::WAVES_K : 0);
+  __shared__ __attribute__((aligned(1024))) char lds[RING > T::LDS ? RING : T::LDS];
 
   const int lane = threadIdx.x & 63;
   const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -382,8 +474,18 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
     la.send(ring + stage * T::STAGE, left_a > 0);
     left_a -= T::WAVES_K;
   };
+  Blocks blocks;
+  const rlds_t scales = (rlds_t)lds + T::RING + kgroup * (Blocks::STAGE * S);
+  if constexpr (M4) {
+    const int row_bytes = (p.K + 15) / 16;
+    blocks.init(p.block_a + row_c * row_bytes, p.block_b + (static_cast<long long>(group) * p.N + n0) * row_bytes,
+                row_bytes, rows, cols, wave, lane);
+    blocks.skip(skip * Blocks::ROW);
+  }
+
   auto send_b = [&](int stage) {
     lb.send(ring + stage * T::STAGE + T::BM * SL, left_b > 0);
+    if constexpr (M4) blocks.send(scales + stage * Blocks::STAGE, left_b > 0, Blocks::ROW * T::WAVES_K);
     left_b -= T::WAVES_K;
   };
 
@@ -406,14 +508,15 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
   const int c4 = lane % PIECES, n4 = cn + 4 * c4;
   const float* const sb_row = ELEM == kElemI8 ? p.scale_b + static_cast<long long>(group) * p.N : nullptr;
   const float* const bias_row =
-      ELEM == kElemI8 && p.bias ? p.bias + static_cast<long long>(group) * p.N : nullptr;
+      BIASED && p.bias ? p.bias + static_cast<long long>(group) * p.N : nullptr;
   float sb4[4] = {}, bias4[4] = {}, scale_m[T::FM] = {};
-  if constexpr (ELEM == kElemI8) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sb4[i] = sb_row[min(n4 + i, p.N - 1)];
+  if constexpr (BIASED)
     if (bias_row)
 #pragma unroll
       for (int i = 0; i < 4; ++i) bias4[i] = bias_row[min(n4 + i, p.N - 1)];
+  if constexpr (ELEM == kElemI8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sb4[i] = sb_row[min(n4 + i, p.N - 1)];
 #pragma unroll
     for (int i = 0; i < T::FM; ++i)
       scale_m[i] = p.scale_a[row_c + min(block_row(i) + lane % MF, rows - 1)];
@@ -422,8 +525,27 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
   auto run = [&](auto blocks) {
     constexpr int NF = decltype(blocks)::value;  // row blocks a wave multiplies
     constexpr bool ALONE = T::WAVES == 1;
-    constexpr int NIA = LoadA::NI, NIB = LoadB::NI;
+    constexpr int NIA = LoadA::NI, NIB = LoadB::NI + NIS;
     ri4 fa[2][NF], fb[2][T::FN];
+    int sa_now[NF], sb_now[T::FN], sa_next[NF], sb_next[T::FN];  // 4-bit codes: the slice's scales, and the next one's
+    auto read_scales = [&](int stage) {
+      if constexpr (M4) {
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+          sa_next[i] = Blocks::word(scales + stage * Blocks::STAGE, block_row(i), lane);
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j)
+          sb_next[j] = Blocks::word(scales + stage * Blocks::STAGE + Blocks::AT_B, bn + j * MF, lane);
+      }
+    };
+    auto turn_scales = [&] {
+      if constexpr (M4) {
+#pragma unroll
+        for (int i = 0; i < NF; ++i) sa_now[i] = sa_next[i];
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j) sb_now[j] = sb_next[j];
+      }
+    };
     auto read = [&](int half, rlds_t stage, int ks) {
 #pragma unroll
       for (int i = 0; i < NF; ++i)
@@ -434,10 +556,10 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
     };
     // Order within a step group: the next group's reads and the loads go
     // between the matrix instructions.
-    auto schedule = [&](auto loads) {
+    auto schedule = [&](auto loads, auto last) {
       constexpr int NM = NF * T::FN * (ELEM == kElemF32 ? 4 : 1), NL = decltype(loads)::value;
       constexpr int RA = A_ALONG ? 1 : ES == 2 ? 2 : 4, RB = B_ALONG ? 1 : ES == 2 ? 2 : 4;
-      constexpr int ND = NF * RA + T::FN * RB;
+      constexpr int ND = NF * RA + T::FN * RB + (M4 && decltype(last)::value ? NF + T::FN : 0);
       // The loads write LDS, so they stay behind the reads: reads go in the
       // first part of the group, loads in the second.
       constexpr int DPART = NL ? (NM * ND + ND + NL - 1) / (ND + NL) : NM, LPART = NM - DPART;
@@ -452,6 +574,8 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
     };
     ragged_barrier<(S - 2) * (NIA + NIB) + NIA, ALONE>();
     read(0, ring, 0);
+    read_scales(0);
+    turn_scales();
     int at = 0;
     // Step group ks of the slice in stage `at` is multiplied from one half of
     // the operand registers while the next one is read to the other half.
@@ -463,6 +587,7 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
         ragged_barrier<(S - 2) * (NIA + NIB), ALONE>();
         __builtin_amdgcn_sched_barrier(0);
         read(0, ring + (at + 1 == S ? 0 : at + 1) * T::STAGE, 0);
+        read_scales(at + 1 == S ? 0 : at + 1);
         send_a(at);
       } else {
         read(1 - half, ring + at * T::STAGE, ks + 1);
@@ -474,9 +599,14 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
 #pragma unroll
       for (int i = 0; i < NF; ++i)
 #pragma unroll
-        for (int j = 0; j < T::FN; ++j) ragged_mma<ELEM, MF>(acc[i][j], fb[half][j], fa[half][i]);
+        for (int j = 0; j < T::FN; ++j) {
+          if constexpr (M4) ragged_mma_blocks<ks, MF>(acc[i][j], fb[half][j], fa[half][i], sb_now[j], sa_now[i]);
+          else ragged_mma<ELEM, MF>(acc[i][j], fb[half][j], fa[half][i]);
+        }
       if constexpr (FORM == kFormNT) __builtin_amdgcn_s_setprio(0);
-      schedule(std::integral_constant<int, (ks == KS - 1 ? NIA : ks == 0 ? NIB : 0)>{});
+      schedule(std::integral_constant<int, (ks == KS - 1 ? NIA : ks == 0 ? NIB : 0)>{},
+               std::integral_constant<bool, ks == KS - 1>{});
+      if constexpr (ks == KS - 1) turn_scales();
     };
     for (int t = 0; t < turns; ++t) {
       step_group(std::integral_constant<int, 0>{});
@@ -492,15 +622,18 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
   // A slice through registers: `left` steps of the reduction from step `done`.
   typename LoadA::Held ha;
   typename LoadB::Held hb;
+  int hs[NIS + !NIS] = {};
   auto fetch = [&](int done, int left) {
     if constexpr (A_ALONG) la.fetch(ha, a + done * ES, done * ES, left * ES, narrow_a, lane);
     else la.fetch(ha, a + done * p.lda, m_bytes, left, narrow_a, lane);
     if constexpr (B_ALONG) lb.fetch(hb, b + done * ES, done * ES, left * ES, narrow_b, lane);
     else lb.fetch(hb, b + done * p.ldb, n0 * ES, left, narrow_b, lane);
+    if constexpr (M4) blocks.fetch(hs, done / 16 - skip * Blocks::ROW, (left + 15) / 16, lane);
   };
   auto put = [&] {
     la.put(ha, ring, lane);
     lb.put(hb, ring + T::BM * SL, lane);
+    if constexpr (M4) blocks.put(hs, scales, lane);
   };
 
   // Rows of fewer than 16 bytes that are reduction steps: every slice goes
@@ -534,6 +667,7 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
       fetch(len - head, head);  // first, for its loads to come back first
       la.base += la.step;
       lb.base += lb.step;
+      if constexpr (M4) blocks.skip(Blocks::ROW * T::WAVES_K);
       left_a -= T::WAVES_K;
       left_b -= T::WAVES_K;
     } else {
@@ -601,6 +735,7 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
   // past 2^24 once, to half a unit in the last place.
   auto value = [&](int bits, float s, float sbc, float bias) {
     if constexpr (ELEM == kElemI8) return static_cast<float>(bits) * (s * sbc) + bias;
+    else if constexpr (M4) return __builtin_bit_cast(float, bits) + bias;
     else return __builtin_bit_cast(float, bits);
   };
   const bool four = n4 + 4 <= p.N;
@@ -657,7 +792,7 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
         else
           __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(ru2, q), to, off[it], 0, 0);
       };
-      if (ELEM != kElemI8 && p.beta != 0.0f) {
+      if (!BIASED && p.beta != 0.0f) {
         Quad old[ITER];
 #pragma unroll
         for (int it = 0; it < ITER; ++it)
@@ -680,7 +815,7 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             v[e] = value(w[it][e], s[it], sb4[e], bias4[e]);
-            if constexpr (ELEM != kElemI8) v[e] *= p.alpha;
+            if constexpr (!BIASED) v[e] *= p.alpha;
           }
           store(it, v);
         }
@@ -696,7 +831,7 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
           for (int e = 0; e < 3; ++e)
             if (n4 + e < p.N) {
               float x = value(v[e], scale, sb4[e], bias4[e]);
-              if constexpr (ELEM != kElemI8) {
+              if constexpr (!BIASED) {
                 x *= p.alpha;
                 if (p.beta != 0.0f) x += p.beta * static_cast<float>(d[e]);
               }
@@ -798,5 +933,6 @@ hipError_t ragged_f32(int form, int shape, const RaggedArgs&, long long grid, hi
 hipError_t ragged_bf16(int form, int shape, const RaggedArgs&, long long grid, hipStream_t);
 hipError_t ragged_f16(int form, int shape, const RaggedArgs&, long long grid, hipStream_t);
 hipError_t ragged_i8(int form, int shape, const RaggedArgs&, long long grid, hipStream_t);
+hipError_t ragged_m4(int form, int shape, const RaggedArgs&, long long grid, hipStream_t);
 
 }  // namespace fp32gemm

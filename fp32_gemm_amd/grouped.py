@@ -1,5 +1,5 @@
-"""Products grouped by expert, their weight gradient, and the 8-bit product
-(include/grouped_gemm.h).  csrc/torch_calls.cpp checks and marshals the tensors.
+"""Products grouped by expert, their weight gradient, and the 8-bit and 4-bit
+products (include/grouped_gemm.h).  csrc/torch_calls.cpp checks and marshals the tensors.
 
 A layer of experts sorts its rows by expert and describes the sorting by
 ``offsets``, an int32 GPU tensor of E + 1 row numbers: expert e owns the rows
@@ -40,6 +40,9 @@ _SIGS = {
     "quantize_rows": ([_i32, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp], ctypes.c_int),
     "igemm": ([_i32, _i32, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64,
                _vp], ctypes.c_int),
+    "quantize_mx4": ([_i32, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp], ctypes.c_int),
+    "gemm_mx4": ([_i32, _i32, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64,
+                  _vp], ctypes.c_int),
     "gemm_grouped_plan": ([_i32, _i32, _i32, _i32, _i64, _i64, _i64, ctypes.POINTER(_i32)], _i64),
     "gemm_grouped_tile": ([_i32, _i32, _i32, _i32, _i64, _i64, _i64], _i32),
     "gemm_grouped_tiles": ([_i32, _i32], _i32),
@@ -52,7 +55,7 @@ for _name, (_args, _res) in _SIGS.items():
     _fn.restype = _res
 
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-_INT8 = {torch.int8: 3}
+_INT8 = {torch.int8: 3, torch.uint8: 5}  # for a plan: igemm's operands, and gemm_mx4's
 _FORMS = {"nt": 0, "nn": 1, "tn": 2}
 
 
@@ -76,9 +79,10 @@ TILES = ("256x256", "128x128", "128x128 deep", "64x64", "16x32", "16x16")
 def plan(form: str, dtype, groups: int, M: int, N: int, K: int, out=None) -> dict:
     """The tile and workgroups of a product; form "nt", "nn" or "tn" as the
     kernels see it (transposed weights, plain weights, weight gradient); out is
-    the output's type (default: the operands', bfloat16 for int8)."""
+    the output's type (default: the operands', bfloat16 for int8 and for uint8,
+    the 4-bit product, whose K counts bytes here)."""
     tile = (_i32 * 2)()
-    out = out or (torch.bfloat16 if dtype is torch.int8 else dtype)
+    out = out or (torch.bfloat16 if dtype in _INT8 else dtype)
     args = (_FORMS[form], {**_TYPES, **_INT8}[dtype], _TYPES[out], groups, M, N, K)
     grid = _lib.gemm_grouped_plan(*args, tile)
     if grid < 0:
@@ -161,4 +165,35 @@ def igemm(A, scale_a, B, scale_b, C, bias=None, offsets=None, stream=None):
     status = _torch_calls.igemm(A, scale_a, B, scale_b, C, bias, offsets, stream)
     if status:
         raise GroupedGemmError("igemm", status)
+    return C
+
+
+def quantize_mx4(X, Q, scale, stream=None):
+    """Bring every row of X (M x K) to microscaled 4-bit floats: Q is uint8,
+    M x (K + 1) // 2, the even column's code in a byte's low half, and scale is
+    uint8, M x (K + 31) // 32, an exponent for each 32 columns.
+
+    A code stands for 0, 1/2, 1, 3/2, 2, 3, 4 or 6 and a sign, times
+    2 ** (scale - 127).  The scale is the exponent of the block's largest
+    magnitude less 2, codes are the nearest, ties to even, at most 6.  A block
+    that holds an infinity or NaN gets scale 255 (NaN) and codes 0.  Returns
+    (Q, scale).
+    """
+    status = _torch_calls.quantize_mx4(X, Q, scale, stream)
+    if status:
+        raise GroupedGemmError("quantize_mx4", status)
+    return Q, scale
+
+
+def gemm_mx4(A, scale_a, B, scale_b, C, bias=None, offsets=None, stream=None):
+    """C[r, n] <- A[r] . B[e, n] + bias[e, n], both in microscaled 4-bit floats.
+
+    A is M x K and B is N x K (E x N x K with ``offsets``) in the form that
+    :func:`quantize_mx4` writes, K two codes a byte; scales belong to rows of
+    either.  bias is float32, N (E x N).  Products are exact, sums float32.  C is
+    float32, bfloat16 or float16.
+    """
+    status = _torch_calls.gemm_mx4(A, scale_a, B, scale_b, C, bias, offsets, stream)
+    if status:
+        raise GroupedGemmError("gemm_mx4", status)
     return C

@@ -1,8 +1,8 @@
 /*
  * grouped_gemm.h -- C ABI of libfp32_gemm_amd.so: matrix products grouped by
- * expert with ragged sizes, their weight gradient, and the product in 8-bit
- * integers with a scale for each token and channel, on one AMD Instinct
- * MI355X (gfx950).
+ * expert with ragged sizes, their weight gradient, the product in 8-bit
+ * integers with a scale for each token and channel, and the product in
+ * microscaled 4-bit floats, on one AMD Instinct MI355X (gfx950).
  *
  * Groups.  The rows of X (A) are sorted by group: group e owns the rows
  * offsets[e] .. offsets[e+1]-1, and is multiplied by its own weights W_e.
@@ -104,9 +104,41 @@ int igemm(int32_t out_type, int32_t groups, const int32_t* offsets, int64_t M, i
           int64_t stride_b, const float* scale_b, const float* bias, void* C, int64_t ldc,
           void* stream);
 
+/* Microscaled 4-bit floats (the public OCP format MXFP4).  Every 32 values that
+ * follow one another in a row share a scale byte s, which stands for 2^(s - 127)
+ * (255: NaN), and are codes of 4 bits: a sign and one of 0, 1/2, 1, 3/2, 2, 3, 4,
+ * 6.  A row of K values is (K + 1) / 2 bytes, the even column in a byte's low half,
+ * and (K + 31) / 32 scales; rows of scales follow one another without gaps. */
+
+/* Brings every row of X (M x K, of `type`) to microscaled 4-bit floats.  A block's
+ * scale is 2^(floor(log2 max|X|) - 2), at least 2^-127, and its codes the nearest
+ * to X / scale, ties to the even code, at most 6.  A block of zeros gets scale byte
+ * 0, a block that holds an infinity or a NaN scale byte 255 and codes 0, so that
+ * its products are NaN throughout.  Where K is odd, the last byte's high half is 0.
+ * Weights are brought to 4 bits by the same call, a channel a row.
+ * -1 type  -2 M  -3 K negative  -4 X  -6 Q  -8 scale NULL while not empty
+ * -5 ldx  -7 ldq (bytes) smaller than a row */
+int quantize_mx4(int32_t type, int64_t M, int64_t K, const void* X, int64_t ldx, uint8_t* Q,
+                 int64_t ldq, uint8_t* scale, void* stream);
+
+/* C[r,n] = sum_k A[r,k] * B_e[n,k] + bias[e,n] for every row r of every group e, A
+ * (M x K) and B_e (N x K) in microscaled 4-bit floats.  lda, ldb and stride_b, the
+ * distance of B_e and B_(e+1), are in bytes; scale_a is M rows of scales, scale_b
+ * groups x N, bias (or NULL) groups x N, all tight.  Products are exact, sums 32-bit
+ * floats, the result is rounded once.  out_type: C's.  K == 0 gives the bias.  Where
+ * K is odd, the high half of a row's last byte counts as one more value.
+ * -1 out_type  -2 groups < 1, or not 1 without offsets  -4 M  -5 N  -6 K
+ * negative  -7 A  -9 scale_a  -10 B  -13 scale_b  -15 C NULL while not empty
+ * -8 lda  -11 ldb  -16 ldc smaller than a row  -12 stride_b < 0 */
+int gemm_mx4(int32_t out_type, int32_t groups, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
+             const uint8_t* A, int64_t lda, const uint8_t* scale_a, const uint8_t* B, int64_t ldb,
+             int64_t stride_b, const uint8_t* scale_b, const float* bias, void* C, int64_t ldc,
+             void* stream);
+
 /* The tile a product would run with, without a device.  form: 0 gemm_grouped
  * and igemm with transposed weights, 1 gemm_grouped with K x N weights, 2
- * gemm_grouped_wgrad; type: GEMM_*, or 3 for igemm; out_type: GEMM_*.  Fills
+ * gemm_grouped_wgrad; type: GEMM_*, 3 for igemm, or 5 for gemm_mx4, whose K counts
+ * bytes here; out_type: GEMM_*.  Fills
  * tile[0..1] with the output tile's rows and columns and returns the number of
  * workgroups, or -1 for arguments out of range. */
 int64_t gemm_grouped_plan(int32_t form, int32_t type, int32_t out_type, int32_t groups, int64_t M,
