@@ -3,13 +3,26 @@
 //   h[t, j] = silu(G_e x_t) * (U_e x_t)   (or silu(U_e x_t)),   e = ids[t, j]
 //   y[t] = sum_j share[t, j] D_e h[t, j]
 //
-// What bounds it is reading the chosen experts' weights, once each.  A wave
-// reads 16 rows of weights, 64 bytes of each a step, straight to registers in the
-// order in which the matrix instruction takes them: a lane's 16 bytes are its
-// operand, so that neither LDS nor a barrier stands between memory and the
-// products.  The expert's tokens, gathered, are the instruction's other operand,
-// up to 16 of them at once; they come out of the L2.  The eight waves of a
-// workgroup divide the reduction and add up in a fixed order.
+// What bounds it is reading the chosen experts' weights, once each.  Both kernels
+// multiply an expert's rows by the gathered values of up to 16 of its tokens.  There
+// is one workgroup a compute unit; each takes an equal run of all the rows that are to
+// be multiplied.  Its eight waves divide the reduction, of 32 rows at a time, or, where
+// it is short, two or four times as many rows as well; they add up in LDS in a fixed
+// order, and load the next rows meanwhile.  A wave reads 16 rows, 64 bytes of each a step, straight to registers in
+// the order in which the matrix instruction takes them: a lane's 16 bytes are its
+// operand, so that neither LDS nor a barrier stands between memory and the products.
+// The tokens' values, the instruction's other operand, stay in registers for all of
+// an expert's rows.
+//
+// Measured, for the layer of 4096 by 2048 with a gate: one token, 2 of 16 experts in
+// bf16 28 us (3.6 TB/s over both kernels), 64 tokens, 16 experts in 8 bits 108 us
+// (3.6 TB/s), in bf16 168 us (4.8 TB/s).  The first kernel streams 5 TB/s once it is
+// under way; each kernel begins with some 8 us of latency (ids, first weights and
+// values) in which it reads little.
+//
+// The second kernel leaves an expert's products, not yet shared out, for each pair
+// of token and choice; the last workgroup to finish a block of columns adds them up
+// for every token, in the order of its choices.
 #include "expert_layer.hpp"
 
 #include "ragged_kernels.hpp"
@@ -18,76 +31,174 @@ namespace fp32gemm {
 namespace {
 
 constexpr int kWaves = 8, kThreads = kWaves * 64, kRows = 16;
+constexpr int kGroups = 256;  // workgroups: one a compute unit
 static_assert(kThreads >= kLayerPairs, "a thread for each pair");
-
-// What the ids say, in LDS.  A token that chose an expert more than once counts
-// once, with the sum of its shares; ids out of range choose nothing.
-struct Routing {
-  int id[kLayerPairs];  // -1: none
-  float share[kLayerPairs];
-  int used[kLayerPairs];  // experts in the order in which the pairs name them
-  int first[kLayerExperts];
-  int count[kWaves];
-};
 
 __device__ __forceinline__ int lanes_below(unsigned long long m) {
   return __builtin_amdgcn_mbcnt_hi(static_cast<unsigned>(m >> 32),
                                    __builtin_amdgcn_mbcnt_lo(static_cast<unsigned>(m), 0));
 }
 
-// Returns how many experts are used.  Every thread of the workgroup takes part.
-__device__ __forceinline__ int find_routing(Routing& r, const LayerArgs& p) {
-  const int i = threadIdx.x, pairs = p.T * p.top, wave = i >> 6;
-  int e = -1;
-  if (i < pairs) {
-    e = p.ids[i];
-    if (e < 0 || e >= p.experts) e = -1;
-    r.id[i] = e;
-    r.share[i] = p.share[i];
-    if (e >= 0) r.first[e] = kLayerPairs;
-  }
-  __syncthreads();
-  const int j = i < pairs ? i % p.top : 0;
-  bool again = false;
-  for (int k = 1; k <= j; ++k) again |= r.id[i - k] == e;
-  if (again) e = -1;
-  float share = 0.0f;
-  if (e >= 0) {
-    atomicMin(&r.first[e], i);  // whatever the order, the least stays
-    for (int k = 0; j + k < p.top; ++k) share += r.id[i + k] == e ? r.share[i + k] : 0.0f;
-  }
-  __syncthreads();
-  const bool leads = e >= 0 && r.first[e] == i;
-  const unsigned long long m = __ballot(leads);
-  if ((i & 63) == 0) r.count[wave] = __builtin_popcountll(m);
-  if (i < pairs) {
-    r.id[i] = e;
-    r.share[i] = share;
-  }
-  __syncthreads();
-  int before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    before += w < wave ? r.count[w] : 0;
-    all += r.count[w];
-  }
-  if (leads) r.used[before + lanes_below(m)] = e;
-  __syncthreads();
-  return all;
-}
+// What the ids say: the experts that any token names, in the order of the pairs
+// (token, choice) that name them first, and each one's pairs.  A token that names
+// an expert more than once counts once; ids out of range name nothing.  An expert
+// whose pairs are more than 16 is taken once for each 16: the entries below.  There
+// are two ways to them.
 
-// The pairs of expert e, in order, by one wave; returns how many.
-__device__ __forceinline__ int list_pairs(const Routing& r, int e, int pairs, short* list, int lane) {
-  int n = 0;
-  for (int i0 = 0; i0 < pairs; i0 += 64) {
-    const bool mine = i0 + lane < pairs && r.id[i0 + lane] == e;
-    const unsigned long long m = __ballot(mine);
-    if (mine) list[n + lanes_below(m)] = static_cast<short>(i0 + lane);
-    n += __builtin_popcountll(m);
+// Up to 128 pairs that name up to 32 experts: every wave finds them by itself, two
+// pairs a lane and a few instructions for each expert.
+constexpr int kFewPairs = 128, kFewExperts = 32;
+struct FewPairs {
+  int id[2];  // of pairs lane and 64 + lane; -1: none
+  int top;
+
+  __device__ __forceinline__ void init(const LayerArgs& p, int lane) {
+    top = p.top;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = 64 * k + lane;
+      const int e = i < p.T * p.top ? p.ids[i] : -1;
+      id[k] = e >= 0 && e < p.experts ? e : -1;
+    }
   }
-  __builtin_amdgcn_wave_barrier();
-  return n;
-}
+  // Calls visit(expert, entries) for one expert after another until it says no.
+  template <class F>
+  __device__ __forceinline__ void walk(F visit) const {
+    unsigned long long left[2] = {__ballot(id[0] >= 0), __ballot(id[1] >= 0)};
+    while (left[0] | left[1]) {
+      const int e = left[0] ? __builtin_amdgcn_readlane(id[0], __builtin_ctzll(left[0]))
+                            : __builtin_amdgcn_readlane(id[1], __builtin_ctzll(left[1]));
+      int n = 0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const unsigned long long m = __ballot(id[k] == e);
+        left[k] &= ~m;
+        n += __builtin_popcountll(m);
+      }
+      if (!visit(e, (n + 15) / 16)) return;
+    }
+  }
+  __device__ __forceinline__ int entries() const {
+    int all = 0;
+    walk([&](int, int n) {
+      all += n;
+      return true;
+    });
+    return all;
+  }
+  // Entry v: its expert, and which 16 of its pairs.
+  __device__ __forceinline__ void entry(int v, int& e, int& set) const {
+    walk([&](int expert, int n) {
+      e = expert;
+      set = v;
+      v -= n;
+      return v >= 0;
+    });
+  }
+  // The pairs of expert e from the first-th on, in order, at most 16; returns how many.
+  __device__ __forceinline__ int list_pairs(int e, int first, short* list, int lane) const {
+    int n = -first;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = 64 * k + lane, j = i % top;
+      bool mine = id[k] == e;
+      for (int d = 1; d < top; ++d) {  // the token's other choices; all lanes fetch
+        const int before0 = __shfl(id[0], i - d & 63), before1 = __shfl(id[1], i - d & 63);
+        if (d <= j && (i - d < 64 ? before0 : before1) == e) mine = false;
+      }
+      const unsigned long long m = __ballot(mine);
+      const int at = n + lanes_below(m);
+      if (mine && at >= 0 && at < 16) list[at] = static_cast<short>(i);
+      n += __builtin_popcountll(m);
+    }
+    __builtin_amdgcn_wave_barrier();
+    return min(max(n, 0), 16);
+  }
+};
+
+// More: a table in LDS, made by the whole workgroup.
+struct Routing {
+  int id[kLayerPairs];    // -1: none, or an earlier choice of the token is the same
+  int used[kLayerPairs];  // experts
+  int upto[kLayerPairs];  // entries of all experts before it, and its own
+  int pairs[kLayerExperts];
+  int first[kLayerExperts];
+  int count[kWaves];
+
+  // Returns how many entries there are.
+  __device__ __forceinline__ int init(const LayerArgs& p) {
+    const int i = threadIdx.x, all = p.T * p.top, wave = i >> 6;
+    int e = -1;
+    if (i < all) {
+      e = p.ids[i];
+      if (e < 0 || e >= p.experts) e = -1;
+      id[i] = e;
+      if (e >= 0) {
+        first[e] = kLayerPairs;
+        pairs[e] = 0;
+      }
+    }
+    __syncthreads();
+    const int j = i < all ? i % p.top : 0;
+    bool again = false;
+    for (int k = 1; k <= j; ++k) again |= id[i - k] == e;
+    if (again) e = -1;
+    if (e >= 0) {  // whatever the order, the least stays and the sum is the same
+      atomicMin(&first[e], i);
+      atomicAdd(&pairs[e], 1);
+    }
+    __syncthreads();
+    const bool leads = e >= 0 && first[e] == i;
+    const unsigned long long m = __ballot(leads);
+    if ((i & 63) == 0) count[wave] = __builtin_popcountll(m);
+    if (i < all) id[i] = e;
+    __syncthreads();
+    int before = 0, experts = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      before += w < wave ? count[w] : 0;
+      experts += count[w];
+    }
+    if (leads) used[before + lanes_below(m)] = e;
+    __syncthreads();
+    const int mine = i < experts ? (pairs[used[i]] + 15) / 16 : 0;
+    const int sum = DeviceWave::sum_below(mine);
+    if ((i & 63) == 63) count[wave] = sum;
+    __syncthreads();
+    before = 0;
+    int entries = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      before += w < wave ? count[w] : 0;
+      entries += count[w];
+    }
+    if (i < kLayerPairs) upto[i] = before + sum;
+    __syncthreads();
+    return entries;
+  }
+  __device__ __forceinline__ void entry(int v, int& e, int& set) const {
+    int lo = 0, hi = kLayerPairs - 1;  // the first expert whose entries go past v
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (upto[mid] > v) hi = mid;
+      else lo = mid + 1;
+    }
+    e = used[lo];
+    set = v - (lo > 0 ? upto[lo - 1] : 0);
+  }
+  __device__ __forceinline__ int list_pairs(int e, int from, int all, short* list, int lane) const {
+    int n = -from;
+    for (int i0 = 0; i0 < all && n < 16; i0 += 64) {
+      const bool mine = i0 + lane < all && id[i0 + lane] == e;
+      const unsigned long long m = __ballot(mine);
+      const int at = n + lanes_below(m);
+      if (mine && at >= 0 && at < 16) list[at] = static_cast<short>(i0 + lane);
+      n += __builtin_popcountll(m);
+    }
+    __builtin_amdgcn_wave_barrier();
+    return min(max(n, 0), 16);
+  }
+};
 
 // ---------------------------------------------------------------------------
 // How weights of format WE and values of type XE are multiplied.
@@ -141,6 +252,17 @@ __device__ __forceinline__ void split_values(const ri4* raw, int m, rb8 (&part)[
   }
 }
 
+// Eight narrow weights, the lowest of `bits`, times eight values.
+template <int XE, int WE>
+__device__ __forceinline__ void layer_mma_8(rf4& acc, int lo, int hi, const ri4* x, int m, float scale) {
+  using Fm = Format<XE, WE>;
+  rb8 wb, part[Fm::PARTS];
+  if constexpr (Fm::BLOCKS) wb = weights_of_4_bits(static_cast<unsigned>(lo), scale);
+  else wb = weights_of_8_bits(lo, hi);
+  split_values<XE, Fm::PARTS>(x, m, part);
+#pragma unroll
+  for (int k = 0; k < Fm::PARTS; ++k) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, part[k], acc, 0, 0, 0);
+}
 // One step of one block of rows and one set of tokens.
 template <int XE, int WE>
 __device__ __forceinline__ void layer_mma(rf4& acc, const ri4& w, const ri4* x, float scale) {
@@ -149,185 +271,264 @@ __device__ __forceinline__ void layer_mma(rf4& acc, const ri4& w, const ri4* x, 
     ragged_mma<XE, 16>(acc, w, x[0]);
   } else {
 #pragma unroll
-    for (int m = 0; m < Fm::MMAS; ++m) {
-      rb8 wb, part[Fm::PARTS];
-      if constexpr (Fm::BLOCKS) wb = weights_of_4_bits(static_cast<unsigned>(w[m]), scale);
-      else wb = weights_of_8_bits(w[2 * m], w[2 * m + 1]);
-      split_values<XE, Fm::PARTS>(x, m, part);
-#pragma unroll
-      for (int k = 0; k < Fm::PARTS; ++k) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, part[k], acc, 0, 0, 0);
-    }
+    for (int m = 0; m < Fm::MMAS; ++m)
+      layer_mma_8<XE, WE>(acc, Fm::BLOCKS ? w[m] : w[2 * m & 3], Fm::BLOCKS ? 0 : w[2 * m + 1 & 3], x, m, scale);
   }
 }
 
-// The reduction over one expert's rows by one wave: NB blocks of 16 rows, NT
-// sets of 16 tokens, U steps on their way at a time and U more in hand.
-template <int XE, int WE, int NB, int NT, int U>
-struct Stream {
+// A wave's part of an expert's rows: NB blocks of 16 rows at a time, U steps of
+// them on their way and U more in hand.
+//   Q > 0   the tokens' values stay in registers for all rows: Q turns of U steps
+//           are all that the wave has of the reduction.
+//   Q == 0  they are loaded again with each turn.
+template <int XE, int WE, int U, int Q, int NB = 2>
+struct Rows {
   using Fm = Format<XE, WE>;
-  static constexpr int BYTES = 64 * U;  // of a row in a turn
+  static constexpr bool KEPT = Q > 0;
+  static constexpr int XT = KEPT ? Q : 1;
+  static constexpr bool AHEAD = KEPT || U * (NB * 4 + Fm::XV * 4) <= 48;  // as far as registers go
   struct Held {
     ri4 w[U][NB];
-    ri4 x[U][NT][Fm::XV];
-    int s[U][NB];
+    int s[U][NB];  // 4-bit codes: the blocks' scales, as loaded
+    ri4 x[KEPT ? 1 : U][Fm::XV];
   };
-  const char* rows[NB];  // the first row of each block
+  const char* rows[NB];    // the expert's first row of each kind of block
   const char* scales[NB];
-  int row_off[NB], scale_off[NB];  // the lane's row past them
-  int x_off[NT];                   // the lane's token past `values`, or kRaggedMasked
   const char* values;
-  int lane, row_bytes, steps;  // bytes of a row, reduction steps of it
+  int lane, last, gap;             // the last row of a block's kind; rows from a set of blocks to the next one
+  int blocks = 1, block0 = 0;      // sets of the workgroup, and the wave's
+  long long ld, scale_ld;          // bytes between rows
+  int row_bytes, steps, full;      // of a row; reduction steps; whole steps of 64 bytes
+  int first_step, end_step, turns; // the wave's steps, and its turns
+  int x_off;                       // the lane's token past `values`, or kRaggedMasked
+  ri4 kept[XT][U][Fm::XV];
+  bool tail;                       // this wave takes what whole steps leave
 
-  // A whole turn.
-  __device__ __forceinline__ void load(Held& h, int turn) const {
-    const int at = turn * BYTES + lane / 16 * 16;
+  __device__ __forceinline__ int row_of(int block, int b) const {
+    return (block * blocks + block0) * gap + (gap == 32 ? 16 * b : 0);
+  }
+  __device__ __forceinline__ int lane_row(int row) const { return min(lane % 16, max(last - row, 0)); }
+  __device__ __forceinline__ int clamped(int row) const { return min(row, last); }
+
+  // The values of `n` tokens come through LDS, a kilobyte of one token's an
+  // instruction: loaded as the products take them, each would touch 64 lines.  Piece c
+  // of token t lies at place c ^ t of its row, so that the tokens' reads spread over
+  // the banks.
+  static constexpr int KEEP_ROW = XT * U * Fm::STEP * Fm::XS;  // bytes of a token
+  static_assert(!KEPT || (KEEP_ROW & (KEEP_ROW - 1)) == 0, "a power of two");
+  __device__ __forceinline__ void send_values(rlds_t room, int n, const short* list, int top, long long ldx) const {
+    constexpr int PIECES = KEEP_ROW / 16, EACH = PIECES < 64 ? 64 / PIECES : 1;  // tokens an instruction
+    const auto v = ragged_rsrc(values, kRaggedMasked);
+    const int end = end_step * Fm::STEP * Fm::XS, start = first_step * Fm::STEP * Fm::XS;
+    for (int t0 = 0; t0 < n; t0 += EACH)
+#pragma unroll
+      for (int part = 0; part < (PIECES + 63) / 64; ++part) {
+        const int t = t0 + (EACH > 1 ? lane / PIECES : 0), place = part * 64 + lane % (EACH > 1 ? PIECES : 64);
+        const int at = start + (place ^ (t & (PIECES - 1) & 15)) * 16;
+        const int row = list[min(t, 15)] / top * static_cast<int>(ldx);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            v, (__attribute__((address_space(3))) void*)(room + t0 * KEEP_ROW + part * 1024), 16,
+            t < n && at < end ? row + at : kRaggedMasked, 0, 0, 0);
+      }
+  }
+  __device__ __forceinline__ void keep_values(rlds_t room, int n) {
+    constexpr int PIECES = KEEP_ROW / 16;
+    const int t = lane % 16;
+#pragma unroll
+    for (int q = 0; q < XT; ++q)
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < Fm::XV; ++i) {
+          const int piece = ((q * U + u) * 4 + lane / 16) * Fm::XV + i;
+          const ri4 x = *(__attribute__((address_space(3))) ri4*)(room + t * KEEP_ROW +
+                                                                 (piece ^ (t & (PIECES - 1) & 15)) * 16);
+          kept[q][u][i] = t < n ? x : ri4{};
+        }
+  }
+  __device__ __forceinline__ void load(Held& h, int block, int turn) const {
+    const int step = first_step + turn * U;
+    const bool whole = step + U <= end_step;  // else steps past the wave's last read as zeros
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const auto r = ragged_rsrc(rows[b], kRaggedMasked);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        h.w[u][b] = __builtin_bit_cast(ri4, __builtin_amdgcn_raw_buffer_load_b128(r, row_off[b] + at, u * 64, 0));
-      if constexpr (Fm::BLOCKS) {
-        const auto q = ragged_rsrc(scales[b], kRaggedMasked);
+      const int row = clamped(row_of(block, b)), in = lane_row(row);
+      const auto r = ragged_rsrc(rows[b] + row * ld + step * 64, kRaggedMasked);
+      const int off = in * static_cast<int>(ld) + lane / 16 * 16;
+      if (whole) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          h.s[u][b] = __builtin_amdgcn_raw_buffer_load_b8(q, scale_off[b] + turn * (U * 4) + lane / 16, u * 4, 0);
+          h.w[u][b] = __builtin_bit_cast(ri4, __builtin_amdgcn_raw_buffer_load_b128(r, off, u * 64, 0));
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          h.w[u][b] = __builtin_bit_cast(
+              ri4, __builtin_amdgcn_raw_buffer_load_b128(r, step + u < end_step ? off : kRaggedMasked, u * 64, 0));
+      }
+      if constexpr (Fm::BLOCKS) {
+        // The scales of four steps are 16 bytes of a row, four for each step, and a
+        // lane's the one of its 32 codes.
+        const auto q = ragged_rsrc(scales[b] + row * scale_ld + step * 4, kRaggedMasked);
+        const int at = in * static_cast<int>(scale_ld);
+        if (U == 4 && whole) {
+          const ri4 w = __builtin_bit_cast(ri4, __builtin_amdgcn_raw_buffer_load_b128(q, at, 0, 0));
+#pragma unroll
+          for (int u = 0; u < U; ++u) h.s[u][b] = w[u & 3];
+        } else {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            h.s[u][b] = static_cast<int>(
+                __builtin_amdgcn_raw_buffer_load_b32(q, step + u < end_step ? at : kRaggedMasked, u * 4, 0));
+        }
       }
     }
-    const auto v = ragged_rsrc(values, kRaggedMasked);
-    const int first = (turn * U * Fm::STEP + lane / 16 * Fm::PER) * Fm::XS;
+    if constexpr (!KEPT) {
+      const auto v = ragged_rsrc(values, kRaggedMasked);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int off = x_off[t] == kRaggedMasked ? kRaggedMasked : x_off[t] + first;
-#pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int u = 0; u < U; ++u) {
+        const int off = x_off == kRaggedMasked || step + u >= end_step
+                            ? kRaggedMasked : x_off + ((step + u) * Fm::STEP + lane / 16 * Fm::PER) * Fm::XS;
 #pragma unroll
         for (int i = 0; i < Fm::XV; ++i)
-          h.x[u][t][i] = __builtin_bit_cast(
-              ri4, __builtin_amdgcn_raw_buffer_load_b128(v, off, (u * Fm::STEP * Fm::XS) + i * 16, 0));
+          h.x[u][i] = __builtin_bit_cast(ri4, __builtin_amdgcn_raw_buffer_load_b128(v, off, i * 16, 0));
+      }
     }
+    __builtin_amdgcn_sched_barrier(0);  // loads go out before anything waits for earlier ones
   }
-  __device__ __forceinline__ void multiply(rf4 (&acc)[NB][NT], const Held& h) const {
+  __device__ __forceinline__ float scale_of(int word) const {
+    return __builtin_bit_cast(float, (word >> (lane / 16 * 8) & 255) << 23);
+  }
+  __device__ __forceinline__ void multiply(rf4 (&acc)[NB], const Held& h, int turn) const {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        float scale = 0.0f;
-        if constexpr (Fm::BLOCKS) scale = __builtin_bit_cast(float, (h.s[u][b] & 255) << 23);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) layer_mma<XE, WE>(acc[b][t], h.w[u][b], h.x[u][t], scale);
+        const float scale = Fm::BLOCKS ? scale_of(h.s[u][b]) : 0.0f;
+        if constexpr (KEPT) layer_mma<XE, WE>(acc[b], h.w[u][b], kept[turn][u], scale);
+        else layer_mma<XE, WE>(acc[b], h.w[u][b], h.x[u], scale);
+        // Or all weights are widened first, in registers that are not there.
+        if constexpr (!Fm::SAME) __builtin_amdgcn_sched_barrier(0);
       }
   }
-  // The last turn, which the rows do not fill: nothing past them is read, and
+  // What whole steps of 64 bytes leave of the rows: nothing past them is read, and
   // what is missing counts as zero.
-  __device__ __forceinline__ void multiply_rest(rf4 (&acc)[NB][NT], int turn) const {
-    const auto v = ragged_rsrc(values, kRaggedMasked);
+  __device__ __forceinline__ void multiply_tail(rf4 (&acc)[NB], int block) const {
+    const int at = full * 64 + lane / 16 * 16, n = row_bytes - at;  // valid bytes from here
+    ri4 w[NB];
+    float scale[NB] = {};
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int row = clamped(row_of(block, b)), in = lane_row(row);
+      const auto r = ragged_rsrc(rows[b] + row * ld, kRaggedMasked);
+      const int off = in * static_cast<int>(ld) + at;
+      if (row_bytes >= 16) {
+        const int back = n > 0 && n < 16 ? 16 - n : 0;
+        const ri4 raw = __builtin_bit_cast(
+            ri4, __builtin_amdgcn_raw_buffer_load_b128(r, n > 0 ? off - back : kRaggedMasked, 0, 0));
+        w[b] = __builtin_bit_cast(ri4, __builtin_bit_cast(unsigned __int128, raw) >> (8 * back));
+      } else {
+        unsigned __int128 bytes = 0;
 #pragma unroll 1
-    for (int u = 0; u < U; ++u) {
-      const int at = turn * BYTES + u * 64 + lane / 16 * 16, n = row_bytes - at;  // valid bytes from here
-      if (turn * BYTES + u * 64 >= row_bytes) break;
-      ri4 w[NB];
-      float scale[NB] = {};
+        for (int i = 0; i < 16; ++i)
+          bytes |= static_cast<unsigned __int128>(
+                       __builtin_amdgcn_raw_buffer_load_b8(r, i < n ? off + i : kRaggedMasked, 0, 0) & 255)
+                   << (8 * i);
+        w[b] = __builtin_bit_cast(ri4, bytes);
+      }
+      if constexpr (Fm::BLOCKS) {
+        const int byte = __builtin_amdgcn_raw_buffer_load_b8(ragged_rsrc(scales[b] + row * scale_ld, kRaggedMasked),
+                                                             n > 0 ? in * static_cast<int>(scale_ld) + at / 16 : kRaggedMasked, 0, 0);
+        scale[b] = __builtin_bit_cast(float, (byte & 255) << 23);
+      }
+    }
+    const auto v = ragged_rsrc(values, kRaggedMasked);
+    const int first = full * Fm::STEP + lane / 16 * Fm::PER;  // the lane's reduction steps
+    // A step's products one after another: written out they would take registers
+    // that the whole steps need.
+    constexpr int PIECES = Fm::SAME ? 1 : 8 * Fm::XS / 16, EACH = 16 / Fm::XS;  // of values, for a product
+#pragma unroll 1
+    for (int m = 0; m < Fm::MMAS; ++m) {
+      ri4 x[PIECES];
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        x[i] = ri4{};
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) {
+          const int step = first + m * 8 + i * EACH + k;
+          const int off = x_off == kRaggedMasked || step >= steps ? kRaggedMasked : x_off + step * Fm::XS;
+          if constexpr (Fm::XS == 4)
+            x[i][k] = static_cast<int>(__builtin_amdgcn_raw_buffer_load_b32(v, off, 0, 0));
+          else
+            x[i][k / 2] |= static_cast<int>(static_cast<unsigned>(__builtin_amdgcn_raw_buffer_load_b16(v, off, 0, 0) & 0xFFFF)
+                                            << (16 * (k & 1)));
+        }
+      }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const auto r = ragged_rsrc(rows[b], kRaggedMasked);
-        if (row_bytes >= 16) {
-          const int back = n > 0 && n < 16 ? 16 - n : 0;
-          const ri4 raw = __builtin_bit_cast(ri4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                     r, n > 0 ? row_off[b] + at - back : kRaggedMasked, 0, 0));
-          w[b] = __builtin_bit_cast(ri4, __builtin_bit_cast(unsigned __int128, raw) >> (8 * back));
-        } else {
-          unsigned __int128 bytes = 0;
-#pragma unroll 1
-          for (int i = 0; i < 16; ++i)
-            bytes |= static_cast<unsigned __int128>(
-                         __builtin_amdgcn_raw_buffer_load_b8(r, i < n ? row_off[b] + at + i : kRaggedMasked, 0, 0) & 255)
-                     << (8 * i);
-          w[b] = __builtin_bit_cast(ri4, bytes);
-        }
-        if constexpr (Fm::BLOCKS) {
-          const int byte = __builtin_amdgcn_raw_buffer_load_b8(ragged_rsrc(scales[b], kRaggedMasked),
-                                                               n > 0 ? scale_off[b] + at / 16 : kRaggedMasked, 0, 0);
-          scale[b] = __builtin_bit_cast(float, (byte & 255) << 23);
-        }
+        if constexpr (Fm::SAME) ragged_mma<XE, 16>(acc[b], w[b], x[0]);
+        else layer_mma_8<XE, WE>(acc[b], w[b][0], w[b][1], x, 0, scale[b]);
+        w[b] = Fm::BLOCKS ? ri4{w[b][1], w[b][2], w[b][3], 0} : ri4{w[b][2], w[b][3], 0, 0};
       }
-      const int first = (turn * U + u) * Fm::STEP + lane / 16 * Fm::PER;  // the lane's reduction steps
+    }
+  }
+  // Blocks lo .. hi - 1; calls end(block, acc) for each, by all waves alike.
+  template <class F>
+  __device__ __forceinline__ void run(int lo, int hi, Held& a, F end) {
+    rf4 acc[NB] = {};
+    Held b;
+    auto done = [&](int block) {
+      if (tail) multiply_tail(acc, block);
+      end(block, acc);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        ri4 x[Fm::XV];
+      for (int i = 0; i < NB; ++i) acc[i] = rf4{};
+    };
+    if constexpr (KEPT) {
+      // The turns of a block, or of two, are written out, so that each knows its
+      // registers.
+      constexpr int BLOCKS = Q % 2 ? 2 : 1;
+      for (int block = lo; block < hi; block += BLOCKS) {
 #pragma unroll
-        for (int i = 0; i < Fm::XV; ++i) {
-          constexpr int EACH = 16 / Fm::XS;
-          x[i] = ri4{};
-#pragma unroll
-          for (int k = 0; k < EACH; ++k) {
-            const int step = first + i * EACH + k;
-            const int off = x_off[t] == kRaggedMasked || step >= steps ? kRaggedMasked : x_off[t] + step * Fm::XS;
-            if constexpr (Fm::XS == 4)
-              x[i][k] = static_cast<int>(__builtin_amdgcn_raw_buffer_load_b32(v, off, 0, 0));
-            else
-              x[i][k / 2] |= static_cast<int>(static_cast<unsigned>(__builtin_amdgcn_raw_buffer_load_b16(v, off, 0, 0) & 0xFFFF)
-                                              << (16 * (k & 1)));
+        for (int i = 0; i < BLOCKS * Q; ++i) {
+          const int now = block + i / Q, next = block + (i + 1) / Q;
+          if (now < hi) {
+            if (next < hi) load(i % 2 ? a : b, next, (i + 1) % Q);
+            multiply(acc, i % 2 ? b : a, i % Q);
+            if (i % Q == Q - 1) done(now);
           }
         }
-#pragma unroll
-        for (int b = 0; b < NB; ++b) layer_mma<XE, WE>(acc[b][t], w[b], x, scale[b]);
+      }
+    } else {
+      for (int block = lo; block < hi; ++block) {
+        int turn = 0;
+        if constexpr (AHEAD) {
+          if (block > lo) load(a, block, 0);
+          for (; turn + 2 < turns; turn += 2) {
+            load(b, block, turn + 1);
+            multiply(acc, a, turn);
+            load(a, block, turn + 2);
+            multiply(acc, b, turn + 1);
+          }
+          if (turn + 1 < turns) {
+            load(b, block, turn + 1);
+            multiply(acc, a, turn);
+            multiply(acc, b, turn + 1);
+          } else {
+            multiply(acc, a, turn);
+          }
+        } else {
+          for (; turn < turns; ++turn) {
+            if (block > lo || turn > 0) load(a, block, turn);
+            multiply(acc, a, turn);
+          }
+        }
+        done(block);
       }
     }
   }
-  // Turns lo .. hi - 1.
-  __device__ __forceinline__ void run(rf4 (&acc)[NB][NT], int lo, int hi) const {
-    const int whole = min(hi, steps / (Fm::STEP * U));  // by the steps: an odd one is half a byte
-    if (lo < whole) {
-      Held a, b;
-      load(a, lo);
-      int t = lo;
-      for (; t + 2 < whole; t += 2) {
-        load(b, t + 1);
-        multiply(acc, a);
-        load(a, t + 2);
-        multiply(acc, b);
-      }
-      if (t + 1 < whole) {
-        load(b, t + 1);
-        multiply(acc, a);
-        multiply(acc, b);
-      } else {
-        multiply(acc, a);
-      }
-    }
-    if (max(lo, whole) < hi) multiply_rest(acc, hi - 1);
-  }
-  static __device__ __forceinline__ int turns(int row_bytes) { return (row_bytes + BYTES - 1) / BYTES; }
 };
 
 template <int WE>
 __device__ __forceinline__ int bytes_of_row(int steps) {
   return WE == kElemM4 ? (steps + 1) / 2 : steps * elem_size(WE);
-}
-// Sets of 16 tokens that share a reading of the weights: four, which is all of
-// them, but one where splitting values takes the registers.
-template <int XE, int WE>
-constexpr int sets_at_once() {
-  return Format<XE, WE>::PARTS == 1 ? 4 : 1;
-}
-// Calls work(sets, first token) for n gathered tokens.
-template <int XE, int WE, class F>
-__device__ __forceinline__ void for_tokens(int n, F work) {
-  if constexpr (sets_at_once<XE, WE>() == 1) {
-    for (int c = 0; c < n; c += 16) work(std::integral_constant<int, 1>{}, c);
-  } else {
-    if (n <= 16) work(std::integral_constant<int, 1>{}, 0);
-    else if (n <= 32) work(std::integral_constant<int, 2>{}, 0);
-    else work(std::integral_constant<int, 4>{}, 0);
-  }
-}
-// Steps on their way at a time: four of 64 bytes, fewer where the values of many
-// tokens, or their parts, fill the registers.
-template <int XE, int WE, int NT>
-constexpr int steps_at_once() {
-  constexpr int values = Format<XE, WE>::XV * NT;
-  return Format<XE, WE>::PARTS > 1 && values >= 4 ? 1 : values <= 4 ? 4 : values <= 8 ? 2 : 1;
 }
 
 __device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
@@ -339,190 +540,394 @@ __device__ __forceinline__ void put(char* p, long long i, float v) {
   else reinterpret_cast<_Float16*>(p)[i] = static_cast<_Float16>(v);
 }
 
+// Products that another workgroup adds up: stored and loaded past the caches that
+// belong to one die (fences in their place write back, or empty, all of an L2: 4 us
+// and more).
+__device__ __forceinline__ void publish(float* p, float v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ rf4 published(const float* p) {
+  typedef float rf2 __attribute__((ext_vector_type(2)));
+  const unsigned long long* const q = reinterpret_cast<const unsigned long long*>(p);
+  const rf2 a = __builtin_bit_cast(rf2, __hip_atomic_load(q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)),
+            b = __builtin_bit_cast(rf2, __hip_atomic_load(q + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+  return {a[0], a[1], b[0], b[1]};
+}
+
+// Meets the other waves once this one's LDS accesses are done; __syncthreads()
+// would also wait for the loads that are on their way.
+__device__ __forceinline__ void meet_in_lds() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // ---------------------------------------------------------------------------
-// h for one used expert (blockIdx.y) and one block of 16 rows of it, gate and up
-// (without a gate: 32 rows).
+// Values that stay in registers: U steps and at most MOST turns of them for a wave, so
+// U MOST XV pieces of 16 bytes of each token's, at most 16, or 8 that take more room
+// once they are split.
 template <int XE, int WE>
-__global__ __launch_bounds__(kThreads, 2) void expert_in_kernel(const LayerArgs p) {
+struct Kept {
+  static constexpr int XV = Format<XE, WE>::XV, PARTS = Format<XE, WE>::PARTS, PIECES = PARTS == 1 ? 16 : 8;
+  static constexpr int U = PIECES / XV < 4 ? PIECES / XV : PARTS == 1 && WE != kElemI8 ? 4 : 2, MOST = PIECES / (U * XV);
+};
+
+// One of the two products.
+template <int XE, int WE, bool IN>
+__global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
+  using Fm = Format<XE, WE>;
+  constexpr int XV = Fm::XV, U = Kept<XE, WE>::U, MOST = Kept<XE, WE>::MOST;
+  // Values that do not: as many steps as registers hold.
+  constexpr int STEP_REGS = 8 + 4 * XV, U0 = STEP_REGS <= 16 ? 4 : STEP_REGS <= 32 ? 2 : 1;
+  __shared__ union {
+    char values[kWaves][16 * MOST * U * Fm::STEP * Fm::XS];
+    float sums[2][kWaves][2][16][kRows + 1];
+    struct {
+      short pair[kLayerPairs];  // of a choice: the pair that holds its products, or -1
+      float share[kLayerPairs];
+    } choice;
+  } lds __attribute__((aligned(1024)));
   __shared__ union {
     Routing routing;
-    float sums[kWaves][2][kLayerTokens][kRows + 1];
-  } lds;
-  __shared__ short list[kLayerTokens];
-  __shared__ int listed;
+    int done[kThreads];  // blocks
+  } table;
+  __shared__ short lists[2][16];
+  __shared__ int listed[2], last_blocks;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int used = find_routing(lds.routing, p);
-  if (static_cast<int>(blockIdx.y) >= used) return;
-  const int e = __builtin_amdgcn_readfirstlane(lds.routing.used[blockIdx.y]);
-  const int pairs = p.T * p.top;
-  if (wave == 0) {
-    const int found = list_pairs(lds.routing, e, pairs, list, lane);
-    if (lane == 0) listed = found;
+  const int depth = IN ? p.D : p.F, wide = IN ? p.F : p.D;  // the reduction, and the outputs of a token
+  const bool gate = IN && p.gated;
+  // Waves that divide the reduction of the same rows, and sets of rows.  A block is all
+  // of a workgroup's rows.
+  const int sets = IN ? p.sets_in : p.sets_out, sharers = kWaves / sets;
+  const int set_of = wave / sharers, sharer = wave - set_of * sharers;
+  const int per = (gate ? 16 : 32) * sets, blocks = (wide + per - 1) / per;
+  if constexpr (IN) {  // for the second kernel, whatever the last call left
+    const int counters = (p.D + 31) / 32;
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < counters; i += gridDim.x * kThreads) p.finished[i] = 0;
+    if (blocks == 0) return;
   }
-  __syncthreads();
-  const int n = __builtin_amdgcn_readfirstlane(listed);
 
-  const int first = blockIdx.x * (p.gated ? kRows : 2 * kRows);
-  const int row_bytes = bytes_of_row<WE>(p.D);
-  const long long blocks = (p.D + 31) / 32;  // scales of a row of 4-bit weights
-  const int rows_of = p.gated ? 2 * p.F : p.F;
-  auto work = [&](auto sets, int c0) {
-    constexpr int NT = decltype(sets)::value, U = steps_at_once<XE, WE, NT>();
-    using S = Stream<XE, WE, 2, NT, U>;
-    S s;
-    s.lane = lane;
-    s.row_bytes = row_bytes;
-    s.steps = p.D;
-    s.values = p.x;
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int f = min(p.gated ? first : first + b * kRows, p.F - 1);
-      const int row = p.gated ? b * p.F + f : f;
-      const int in = min(lane % 16, p.F - 1 - f);
-      s.rows[b] = p.w_in + e * p.stride_in + row * p.ldw_in;
-      s.row_off[b] = in * static_cast<int>(p.ldw_in);
-      s.scales[b] = static_cast<const char*>(p.scale_in) + (static_cast<long long>(e) * rows_of + row) * blocks;
-      s.scale_off[b] = in * static_cast<int>(blocks);
+  FewPairs few;
+  int entries;
+  if (p.few) {
+    few.init(p, lane);
+    entries = few.entries();
+  } else {
+    entries = table.routing.init(p);
+  }
+  entries = __builtin_amdgcn_readfirstlane(entries);
+  // This workgroup's units, a block of an entry each; where nothing is used, y alone
+  // is left to be written, block by block.  Each entry that a workgroup begins costs
+  // it a few microseconds of latency, so the entries get whole workgroups where that
+  // leaves few over (32 experts, 16 tokens, 4 choices, 8 bits, 2048 by 1024: 94 us
+  // with units in equal runs whatever the entry).
+  const int owners = max(entries, IN ? 0 : 1), group = blockIdx.x;
+  const int each = owners > 0 ? kGroups / owners : 0;
+  int begin = 0, end = 0;  // fewer than 2^24 in all: 512 entries of 2^15 blocks
+  if (each * owners * 8 >= kGroups * 7) {
+    const int v = group / each, part = group - v * each;
+    if (v < owners) {
+      begin = v * blocks + blocks * part / each;
+      end = v * blocks + blocks * (part + 1) / each;
     }
+  } else {
+    const long long all = owners * blocks;
+    begin = static_cast<int>(all * group / kGroups);
+    end = static_cast<int>(all * (group + 1) / kGroups);
+  }
+  const int rows_of = gate ? 2 * wide : wide;
+  const int scale_blocks = (depth + 31) / 32;
+  const void* const scale_all = IN ? p.scale_in : p.scale_out;
+
+  int turn_of_list = 0;
+  for (int unit = begin; entries > 0 && unit < end;) {
+    const int v = unit / blocks, lo = unit - v * blocks, hi = min(blocks, lo + (end - unit));
+    unit += hi - lo;
+    int e = 0, set = 0;
+    if (p.few) few.entry(v, e, set);
+    else table.routing.entry(v, e, set);
+    e = __builtin_amdgcn_readfirstlane(e);
+    set = __builtin_amdgcn_readfirstlane(set);
+    short* const list = lists[turn_of_list];
+    auto find = [&] {
+      if (wave == 0) {
+        const int found = p.few ? few.list_pairs(e, 16 * set, list, lane)
+                                : table.routing.list_pairs(e, 16 * set, p.T * p.top, list, lane);
+        if (lane == 0) listed[turn_of_list] = found;
+      }
+      meet_in_lds();
+      return __builtin_amdgcn_readfirstlane(listed[turn_of_list]);
+    };
+    const float* const row_scale = static_cast<const float*>(scale_all) + static_cast<long long>(e) * rows_of;
+
+    auto work = [&](auto us, auto qs) {
+      using R = Rows<XE, WE, decltype(us)::value, decltype(qs)::value>;
+      R r;
+      r.lane = lane;
+      r.ld = IN ? p.ldw_in : p.ldw_out;
+      r.scale_ld = scale_blocks;
+      r.last = wide - 1;
+      r.gap = gate ? 16 : 32;
+      r.row_bytes = bytes_of_row<WE>(depth);
+      r.steps = depth;
+      r.full = depth / Fm::STEP;
+      // The waves take equal runs of whole steps, and the last one what is left.
+      constexpr int UR = decltype(us)::value;
+      r.turns = max((r.full + UR * sharers - 1) / (UR * sharers), 1);
+      r.first_step = sharer * r.turns * UR;
+      r.end_step = min(r.full, r.first_step + r.turns * UR);
+      r.tail = r.full * Fm::STEP < depth && sharer == sharers - 1;
+      r.blocks = sets;
+      r.block0 = set_of;
+      r.values = IN ? p.x : p.h;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int c = c0 + t * 16 + lane % 16;
-      s.x_off[t] = c < n ? list[min(c, kLayerTokens - 1)] / p.top * static_cast<int>(p.ldx) : kRaggedMasked;
+      for (int b = 0; b < 2; ++b) {
+        const long long row = gate ? b * static_cast<long long>(wide) : 0;
+        r.rows[b] = (IN ? p.w_in + e * p.stride_in : p.w_out + e * p.stride_out) + row * r.ld;
+        r.scales[b] = static_cast<const char*>(scale_all) + (static_cast<long long>(e) * rows_of + row) * scale_blocks;
+      }
+      typename R::Held held;
+      if constexpr (R::KEPT) r.load(held, lo, 0);  // weights first, they take longest
+      const int n = find();
+      const int pair = list[lane % 16 < n ? lane % 16 : 0];
+      r.x_off = lane % 16 >= n ? kRaggedMasked
+                : IN           ? pair / p.top * static_cast<int>(p.ldx)
+                               : pair * static_cast<int>(p.ldh);
+      if constexpr (R::KEPT) {
+        const rlds_t room = (rlds_t)&lds.values[wave][0];
+        r.send_values(room, n, list, IN ? p.top : 1, IN ? p.ldx : p.ldh);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        r.keep_values(room, n);
+        meet_in_lds();  // sums may take their place
+      } else {
+        r.load(held, lo, 0);
+      }
+      r.run(lo, hi, held, [&](int block, rf4 (&acc)[2]) {
+        float (&sums)[kWaves][2][16][kRows + 1] = lds.sums[block & 1];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sums[wave][b][lane % 16][lane / 16 * 4 + i] = acc[b][i];
+        meet_in_lds();
+        for (int i = threadIdx.x; i < n * kRows * sets; i += kThreads) {
+          const int row = i % kRows, c = i / kRows % n, first = i / kRows / n;
+          const int to = list[c], base = block * sets + first;
+          float v[2] = {};
+          for (int w = first * sharers; w < (first + 1) * sharers; ++w)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) v[b] += sums[w][b][c][row];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const int out = gate ? base * 16 + row : base * 32 + b * 16 + row;
+            if (out >= wide) break;
+            if constexpr (WE == kElemI8) v[b] *= row_scale[gate ? b * wide + out : out];
+            if constexpr (!IN) publish(p.z + to * p.ldz + out, v[b]);
+            else if (!gate) put<XE>(p.h + to * p.ldh, out, silu(v[b]));
+            else if (b == 1) put<XE>(p.h + to * p.ldh, out, silu(v[0]) * v[1]);
+          }
+        }
+      });
+      meet_in_lds();  // the sums are read: values or other sums may take their place
+    };
+    using std::integral_constant;
+    const int turns = (depth / Fm::STEP + U * sharers - 1) / (U * sharers);
+    const integral_constant<int, U> kept_steps;
+    if (turns > MOST) work(integral_constant<int, U0>{}, integral_constant<int, 0>{});
+    else if (MOST == 1 || turns <= 1) work(kept_steps, integral_constant<int, 1>{});
+    else if (MOST == 2 || turns <= 2) work(kept_steps, integral_constant<int, MOST >= 2 ? 2 : 1>{});
+    else work(kept_steps, integral_constant<int, MOST >= 4 ? 4 : 1>{});
+    turn_of_list ^= 1;
+  }
+
+  if constexpr (!IN) {
+    // The last workgroup at a block of columns adds up each token's choices.  The
+    // products are where every die sees them once the stores are done, which each
+    // wave waits for before the barrier.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if (threadIdx.x == 0) last_blocks = 0;
+    __syncthreads();
+    const int mine = end - begin;
+    for (int i = threadIdx.x; i < mine; i += kThreads) {
+      const int block = (begin + i) % blocks;
+      if (entries == 0 || atomicAdd(&p.finished[block], 1) == entries - 1) {
+        const int at = atomicAdd(&last_blocks, 1);
+        if (at < kThreads) table.done[at] = block;
+      }
     }
-    rf4 acc[2][NT] = {};
-    const int turns = S::turns(row_bytes);
-    s.run(acc, turns * wave / kWaves, turns * (wave + 1) / kWaves);
+    const int pairs = p.T * p.top;
+    for (int i = threadIdx.x; i < pairs; i += kThreads) {
+      const int e = p.ids[i], t = i / p.top;
+      int k = i;
+      if (e >= 0 && e < p.experts)
+        for (k = t * p.top; p.ids[k] != e; ++k) {}
+      else
+        k = -1;
+      lds.choice.pair[i] = static_cast<short>(k);
+      lds.choice.share[i] = p.share[i];
+    }
+    __syncthreads();
+    if (last_blocks == 0) return;
+    // Four columns a thread and four such at a time, so that their loads overlap.
+    const int row_quads = per / 4, quads = last_blocks * row_quads * p.T;  // token by token within a block
+    for (int i0 = threadIdx.x; i0 < quads; i0 += 4 * kThreads) {
+      const float* from[4];
+      int col[4], token[4];
+      rf4 y[4] = {};
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+      for (int k = 0; k < 4; ++k) {
+        const int i = min(i0 + k * kThreads, quads - 1);
+        token[k] = i / row_quads % p.T;
+        col[k] = table.done[i / (row_quads * p.T)] * per + i % row_quads * 4;
+        from[k] = p.z + min(col[k], (wide - 1) / 4 * 4);  // rows of z are whole lines
+      }
+      for (int j0 = 0; j0 < p.top; j0 += 2) {
+        rf4 z[2][4];
+        float share[2][4];
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          lds.sums[wave][b][c0 + t * 16 + lane % 16][lane / 16 * 4 + i] = acc[b][t][i];
-  };
-  for_tokens<XE, WE>(n, work);
-  __syncthreads();
-  for (int i = threadIdx.x; i < n * kRows; i += kThreads) {
-    const int c = i / kRows, row = i % kRows;
-    float v[2] = {};
+          for (int k = 0; k < 4; ++k) {
+            const int c = token[k] * p.top + min(j0 + j, p.top - 1), pair = lds.choice.pair[c];
+            const bool there = pair >= 0 && j0 + j < p.top;
+            share[j][k] = there ? lds.choice.share[c] : 0.0f;
+            z[j][k] = published(from[k] + (there ? pair : 0) * p.ldz);
+            if (!there) z[j][k] = rf4{};
+          }
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) v[b] += lds.sums[w][b][c][row];
-    char* const h = p.h + list[c] * p.ldh;
-    const float* const scale = static_cast<const float*>(p.scale_in) + static_cast<long long>(e) * rows_of;
+          for (int k = 0; k < 4; ++k) y[k] += share[j][k] * z[j][k];
+      }
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int f = p.gated ? first + row : first + b * kRows + row;
-      if (f >= p.F) break;
-      if constexpr (WE == kElemI8) v[b] *= scale[p.gated ? b * p.F + f : f];
-      if (!p.gated) put<XE>(h, f, silu(v[b]));
-      else if (b == 1) put<XE>(h, f, silu(v[0]) * v[1]);
+      for (int k = 0; k < 4; ++k) {
+        if (i0 + k * kThreads >= quads) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (col[k] + i >= wide) break;
+          const long long at = token[k] * p.ldy + col[k] + i;
+          if (XE == kElemF32 || p.out32) put<kElemF32>(p.y, at, y[k][i]);
+          else put<XE>(p.y, at, y[k][i]);
+        }
+      }
     }
   }
 #endif
 }
 
-// 16 columns of y for all tokens.  The waves divide the used experts' rows, end
-// to end; what each finds for a token it adds up in LDS.
+// The second product where few experts are used: a workgroup takes 16 columns of y
+// for all tokens, its waves divide the used experts' rows, end to end, and what each
+// finds for a token it adds up in LDS.  No workgroup waits for another's products
+// (one token, 2 of 16 experts, bf16, 4096 by 2048: the layer takes 28 us so, 33 with
+// the kernel above); with more experts than waves each wave has too many short
+// pieces (8 tokens, 2 choices of 32: 24 us and 19).
+constexpr int kDirectPairs = 8;
 template <int XE, int WE>
 __global__ __launch_bounds__(kThreads, 2) void expert_out_kernel(const LayerArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
-  __shared__ Routing routing;
-  __shared__ float sums[kWaves][kLayerTokens][kRows + 1];
-  __shared__ short list[kWaves][kLayerTokens];
+  using Fm = Format<XE, WE>;
+  constexpr int STEP_REGS = 4 + 4 * Fm::XV, U = STEP_REGS <= 8 ? 8 : STEP_REGS <= 16 ? 4 : STEP_REGS <= 24 ? 2 : 1;
+  using R = Rows<XE, WE, U, 0, 1>;
+  __shared__ float sums[kWaves][kDirectPairs][kRows + 1];
+  __shared__ short lists[kWaves][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  for (int i = threadIdx.x; i < kWaves * kLayerTokens * (kRows + 1); i += kThreads) (&sums[0][0][0])[i] = 0.0f;
-  const int used = __builtin_amdgcn_readfirstlane(find_routing(routing, p));  // ends with a barrier
-  const int pairs = p.T * p.top;
-  const int first = blockIdx.x * kRows, in = min(lane % 16, p.D - 1 - first);
-  const int row_bytes = bytes_of_row<WE>(p.F);
-  const long long blocks = (p.F + 31) / 32;
-  // A turn of the shared division is four steps.
-  constexpr int BYTES = 256;
-  const int turns = (row_bytes + BYTES - 1) / BYTES;
-  const long long all = static_cast<long long>(turns) * used;
-  const int lo = static_cast<int>(all * wave / kWaves), hi = static_cast<int>(all * (wave + 1) / kWaves);
-  for (int u = lo / max(turns, 1); u * turns < hi; ++u) {
-    const int e = __builtin_amdgcn_readfirstlane(routing.used[u]);
-    const int from = max(lo - u * turns, 0), to = min(hi - u * turns, turns);
-    const int n = __builtin_amdgcn_readfirstlane(list_pairs(routing, e, pairs, list[wave], lane));
-    auto work = [&](auto sets, int c0) {
-      constexpr int NT = decltype(sets)::value, U = steps_at_once<XE, WE, NT>();
-      using S = Stream<XE, WE, 1, NT, U>;
-      S s;
-      s.lane = lane;
-      s.row_bytes = row_bytes;
-      s.steps = p.F;
-      s.values = p.h;
-      s.rows[0] = p.w_out + e * p.stride_out + first * p.ldw_out;
-      s.row_off[0] = in * static_cast<int>(p.ldw_out);
-      s.scales[0] = static_cast<const char*>(p.scale_out) + (static_cast<long long>(e) * p.D + first) * blocks;
-      s.scale_off[0] = in * static_cast<int>(blocks);
+  FewPairs few;
+  few.init(p, lane);
+  for (int i = lane; i < kDirectPairs * (kRows + 1); i += 64) (&sums[wave][0][0])[i] = 0.0f;
+  short* const list = lists[wave];
+  const int entries = __builtin_amdgcn_readfirstlane(few.entries());
+  const int block = blockIdx.x, scale_blocks = (p.F + 31) / 32;
+  const int full = p.F / Fm::STEP, turns = max((full + U - 1) / U, 1);
+  const int lo = turns * entries * wave / kWaves, hi = turns * entries * (wave + 1) / kWaves;
+  for (int at = lo; at < hi;) {
+    const int v = at / turns, from = at - v * turns, to = min(turns, from + (hi - at));
+    at += to - from;
+    int e = 0, set = 0;
+    few.entry(v, e, set);
+    e = __builtin_amdgcn_readfirstlane(e);
+    const int n = __builtin_amdgcn_readfirstlane(few.list_pairs(e, 0, list, lane));
+    const int pair = list[lane % 16 < n ? lane % 16 : 0], token = pair / p.top;
+    float share = 0.0f;  // of all the token's choices of e
+    for (int j = token * p.top; j < (token + 1) * p.top; ++j) share += p.ids[j] == e ? p.share[j] : 0.0f;
+    R r;
+    r.lane = lane;
+    r.ld = p.ldw_out;
+    r.scale_ld = scale_blocks;
+    r.last = p.D - 1;
+    r.gap = 16;
+    r.row_bytes = bytes_of_row<WE>(p.F);
+    r.steps = p.F;
+    r.full = full;
+    r.turns = to - from;
+    r.first_step = from * U;
+    r.end_step = min(full, to * U);
+    r.tail = to == turns && full * Fm::STEP < p.F;
+    r.values = p.h;
+    r.rows[0] = p.w_out + e * p.stride_out;
+    r.scales[0] = static_cast<const char*>(p.scale_out) + static_cast<long long>(e) * p.D * scale_blocks;
+    r.x_off = lane % 16 < n ? pair * static_cast<int>(p.ldh) : kRaggedMasked;
+    float scale[4];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int c = c0 + t * 16 + lane % 16;
-        s.x_off[t] = c < n ? list[wave][min(c, kLayerTokens - 1)] * static_cast<int>(p.ldh) : kRaggedMasked;
-      }
-      rf4 acc[1][NT] = {};
-      constexpr int PER = BYTES / S::BYTES;
-      s.run(acc, from * PER, min(to * PER, S::turns(row_bytes)));
-      float scale[4];
+    for (int i = 0; i < 4; ++i)
+      scale[i] = WE == kElemI8 ? static_cast<const float*>(p.scale_out)[static_cast<long long>(e) * p.D +
+                                                                        min(block * 16 + lane / 16 * 4 + i, p.D - 1)]
+                               : 1.0f;
+    typename R::Held held;
+    r.load(held, block, 0);
+    r.run(block, block + 1, held, [&](int, rf4 (&acc)[1]) {
+      if (lane % 16 < n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        scale[i] = WE == kElemI8 ? static_cast<const float*>(p.scale_out)[static_cast<long long>(e) * p.D +
-                                                                          min(first + lane / 16 * 4 + i, p.D - 1)]
-                                 : 1.0f;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int c = c0 + t * 16 + lane % 16;
-        if (c < n) {
-          const int pair = list[wave][c];
-          float* const to_sum = &sums[wave][pair / p.top][lane / 16 * 4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) to_sum[i] += acc[0][t][i] * scale[i] * routing.share[pair];
-        }
-      }
-    };
-    for_tokens<XE, WE>(n, work);
+        for (int i = 0; i < 4; ++i) sums[wave][token][lane / 16 * 4 + i] += acc[0][i] * scale[i] * share;
+    });
     __builtin_amdgcn_wave_barrier();
   }
   __syncthreads();
   for (int i = threadIdx.x; i < p.T * kRows; i += kThreads) {
-    const int t = i / kRows, row = i % kRows;
-    if (first + row >= p.D) continue;
-    float v = 0.0f;
+    const int t = i / kRows, col = block * 16 + i % kRows;
+    if (col >= p.D) continue;
+    float y = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += sums[w][t][row];
-    if (XE == kElemF32 || p.out32) put<kElemF32>(p.y, t * p.ldy + first + row, v);
-    else put<XE>(p.y, t * p.ldy + first + row, v);
+    for (int w = 0; w < kWaves; ++w) y += sums[w][t][i % kRows];
+    if (XE == kElemF32 || p.out32) put<kElemF32>(p.y, t * p.ldy + col, y);
+    else put<XE>(p.y, t * p.ldy + col, y);
   }
 #endif
 }
 
 template <int XE, int WE>
-hipError_t launch_layer(const LayerArgs& args, hipStream_t s) {
+hipError_t launch_tokens(const LayerArgs& args, hipStream_t s) {
   LayerArgs a = args;
   void* values[] = {&a};
-  const unsigned per = a.gated ? kRows : 2 * kRows;
-  const int pairs = a.T * a.top;
-  const unsigned slots = static_cast<unsigned>(pairs < a.experts ? pairs : a.experts);
-  if (slots > 0 && a.F > 0) {
-    const hipError_t err =
-        hipLaunchKernel(reinterpret_cast<const void*>(&expert_in_kernel<XE, WE>),
-                        dim3((static_cast<unsigned>(a.F) + per - 1) / per, slots), dim3(kThreads), values, 0, s);
-    if (err != hipSuccess) return err;
-  }
-  return hipLaunchKernel(reinterpret_cast<const void*>(&expert_out_kernel<XE, WE>),
-                         dim3((static_cast<unsigned>(a.D) + kRows - 1) / kRows), dim3(kThreads), values, 0, s);
+  const int pairs = a.T * a.top, slots = pairs < a.experts ? pairs : a.experts;
+  a.few = pairs <= kFewPairs && slots <= kFewExperts;
+  // Rows beside each other where few waves hold the reduction's values and there are
+  // rows for two blocks a workgroup all the same.
+  auto sets = [&](int depth, int wide, int per) {
+    const int steps = depth / Format<XE, WE>::STEP, hold = Kept<XE, WE>::U * Kept<XE, WE>::MOST;
+    int n = 1;
+    while (n < 4 && steps * 2 * n <= hold * kWaves &&
+           static_cast<long long>(wide) * slots >= 2LL * kGroups * per * 2 * n)
+      n *= 2;
+    return n;
+  };
+  a.sets_in = sets(a.D, a.F, a.gated ? 16 : 32);
+  a.sets_out = sets(a.F, a.D, 32);
+  const hipError_t err = hipLaunchKernel(reinterpret_cast<const void*>(&expert_kernel<XE, WE, true>), dim3(kGroups),
+                                         dim3(kThreads), values, 0, s);
+  if (err != hipSuccess) return err;
+  if (pairs <= kDirectPairs)
+    return hipLaunchKernel(reinterpret_cast<const void*>(&expert_out_kernel<XE, WE>),
+                           dim3((static_cast<unsigned>(a.D) + kRows - 1) / kRows), dim3(kThreads), values, 0, s);
+  return hipLaunchKernel(reinterpret_cast<const void*>(&expert_kernel<XE, WE, false>), dim3(kGroups), dim3(kThreads),
+                         values, 0, s);
 }
 
 template <int XE>
 hipError_t launch_type(int weights, const LayerArgs& a, hipStream_t s) {
-  if (weights == kElemI8) return launch_layer<XE, kElemI8>(a, s);
-  if (weights == kElemM4) return launch_layer<XE, kElemM4>(a, s);
-  return launch_layer<XE, XE>(a, s);
+  if (weights == kElemI8) return launch_tokens<XE, kElemI8>(a, s);
+  if (weights == kElemM4) return launch_tokens<XE, kElemM4>(a, s);
+  return launch_tokens<XE, XE>(a, s);
 }
 
 }  // namespace

@@ -13,16 +13,19 @@ struct LayerArgs {
   const char* w_out;   // experts of D rows of F
   const void* scale_in;   // 8-bit weights: floats, a row each; 4-bit: bytes, a block each
   const void* scale_out;
-  char* h;  // T * top rows of F, of x's type, ldh apart
+  char* h;        // workspace: T * top rows of F, of x's type, ldh apart,
+  float* z;       // T * top rows of D, ldz apart,
+  int* finished;  // and how often each 32 columns of those are done
   char* y;
   long long ldx, ldw_in, ldw_out, ldh;   // bytes
   long long stride_in, stride_out;       // bytes between experts
-  long long ldy;                         // elements
+  long long ldy, ldz;                    // elements
   int T, D, F, experts, top, gated, out32;
+  int few, sets_in, sets_out;  // set by expert_layer_launch
 };
 
 // Tokens, and tokens times experts of each, that one call takes.
-constexpr int kLayerTokens = 64, kLayerPairs = 512, kLayerExperts = 4096;
+constexpr int kLayerTokens = 64, kLayerPairs = 512, kLayerExperts = 1024;
 
 // type: Elem of x and h; weights: Elem of the weights (type, kElemI8 or kElemM4).
 hipError_t expert_layer_launch(int type, int weights, const LayerArgs& a, hipStream_t s);

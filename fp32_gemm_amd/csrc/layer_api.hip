@@ -29,8 +29,20 @@ int launched(hipError_t err) {
   return SGEMM_ERR_LAUNCH;
 }
 
-// Rows of h in the workspace start at multiples of 16 bytes.
-long long layer_row(int type, long long F) { return (F * elem_size(type) + 15) / 16 * 16; }
+// The workspace of a layer: rows of h, rows of products and a counter for each run
+// of columns, each part and row at a multiple of 128 bytes, a line of the L2's.
+constexpr long long kLine = 128;
+struct LayerRoom {
+  long long h_row, z_row, z, counters, all;  // bytes
+  LayerRoom(int type, long long T, long long D, long long F, long long top) {
+    const auto lines = [](long long n) { return (n + kLine - 1) / kLine * kLine; };
+    h_row = lines(F * elem_size(type));
+    z_row = lines(4 * D);
+    z = T * top * h_row;
+    counters = z + T * top * z_row;
+    all = counters + lines(4 * ((D + 31) / 32));
+  }
+};
 
 }  // namespace
 }  // namespace fp32gemm
@@ -191,7 +203,7 @@ int expert_layer(int32_t type, int32_t weights, int32_t out_type, int32_t gated,
       ldx >= kRaggedMaxLd || ldw_in >= kRaggedMaxLd || ldw_out >= kRaggedMaxLd || ldy >= kRaggedMaxLd ||
       stride_in > kMaxStride || stride_out > kMaxStride)
     return SGEMM_ERR_UNSUPPORTED;
-  const long long room = some ? expert_layer_workspace(type, T, F, top) : 0;
+  const long long room = some ? expert_layer_workspace(type, T, D, F, top) : 0;
   if (room > 0 && (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 16 != 0)) return -24;
   if (workspace_bytes < room) return -25;
   const int es = elem_size(type), wes = i8 || m4 ? 1 : es;
@@ -221,12 +233,16 @@ int expert_layer(int32_t type, int32_t weights, int32_t out_type, int32_t gated,
   a.w_out = static_cast<const char*>(W_out);
   a.scale_in = scale_in;
   a.scale_out = scale_out;
+  const LayerRoom parts(type, T, D, F, top);
   a.h = static_cast<char*>(workspace);
+  a.z = reinterpret_cast<float*>(a.h + parts.z);
+  a.finished = reinterpret_cast<int*>(a.h + parts.counters);
   a.y = static_cast<char*>(Y);
   a.ldx = ldx * es;
   a.ldw_in = ldw_in * wes;
   a.ldw_out = ldw_out * wes;
-  a.ldh = layer_row(type, F);
+  a.ldh = parts.h_row;
+  a.ldz = parts.z_row / 4;
   a.stride_in = stride_in * wes;
   a.stride_out = stride_out * wes;
   a.ldy = ldy;
@@ -240,10 +256,11 @@ int expert_layer(int32_t type, int32_t weights, int32_t out_type, int32_t gated,
   return launched(expert_layer_launch(type, weights, a, static_cast<hipStream_t>(stream)));
 }
 
-int64_t expert_layer_workspace(int32_t type, int64_t T, int64_t F, int32_t top) {
-  if (!float_type(type) || T < 0 || F < 0 || top < 1 || T > kLayerTokens || T * top > kLayerPairs || F > kMaxWidth)
+int64_t expert_layer_workspace(int32_t type, int64_t T, int64_t D, int64_t F, int32_t top) {
+  if (!float_type(type) || T < 0 || D < 0 || F < 0 || top < 1 || T > kLayerTokens || T * top > kLayerPairs ||
+      D > kMaxWidth || F > kMaxWidth)
     return -1;
-  return T * top * layer_row(type, F);
+  return T == 0 || D == 0 ? 0 : LayerRoom(type, T, D, F, top).all;
 }
 
 const char* layer_status_string(int status) {

@@ -460,7 +460,7 @@ PyObject* call_expert_layer(PyObject*, PyObject* const* v, Py_ssize_t n) {
     }
     void* const stream = stream_of(v[10], dev);
     On on(dev);
-    const Workspace room(v[9], expert_layer_workspace(x.code, x.rows, hidden, static_cast<int32_t>(top)), dev, stream);
+    const Workspace room(v[9], expert_layer_workspace(x.code, x.rows, x.cols, hidden, static_cast<int32_t>(top)), dev, stream);
     return expert_layer(x.code, in.code, y.code, gated, x.rows, x.cols, hidden, static_cast<int32_t>(in.groups),
                         static_cast<int32_t>(top), x.data, x.ld, ids, share, in.data, in.ld, in.stride, scale_in,
                         out.data, out.ld, out.stride, scale_out, y.data, y.ld, room.data, room.bytes, stream);

@@ -21,7 +21,7 @@ _SIGS = {
     "rms_norm_grad_workspace": ([_i64, _i64], _i64),
     "expert_layer": ([_i32, _i32, _i32, _i32, _i64, _i64, _i64, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _vp,
                       _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp], ctypes.c_int),
-    "expert_layer_workspace": ([_i32, _i64, _i64, _i32], _i64),
+    "expert_layer_workspace": ([_i32, _i64, _i64, _i64, _i32], _i64),
     "layer_status_string": ([ctypes.c_int], ctypes.c_char_p),
 }
 for _name, (_args, _res) in _SIGS.items():
@@ -101,9 +101,9 @@ def expert_layer(X, ids, share, W_in, W_out, Y, scale_in=None, scale_out=None, g
 
 
 def expert_layer_workspace(X, ids, F: int) -> int:
-    """Bytes of the workspace that :func:`expert_layer` needs for h of F values."""
+    """Bytes of the workspace that :func:`expert_layer` needs with a hidden width of F."""
     from .grouped import _TYPES
-    need = _lib.expert_layer_workspace(_TYPES[X.dtype], X.shape[0], F, ids.shape[1])
+    need = _lib.expert_layer_workspace(_TYPES[X.dtype], X.shape[0], X.shape[1], F, ids.shape[1])
     if need < 0:
         raise ValueError("bad arguments")
     return need

@@ -27,7 +27,7 @@ extern "C" {
 #endif
 
 /* Limits (SGEMM_ERR_UNSUPPORTED beyond): M, K, leading dimensions <= 2^30 for the
- * norms; for expert_layer T <= 64, T * top <= 512, experts <= 4096, D, F <= 2^19,
+ * norms; for expert_layer T <= 64, T * top <= 512, experts <= 1024, D, F <= 2^19,
  * leading dimensions < 2^21, strides <= 2^40. */
 
 /* H = X + R,  Y[r,k] = H[r,k] * s_r * weight[k] with s_r = 1 / sqrt(mean_k H[r,k]^2 + eps),
@@ -78,7 +78,7 @@ int64_t rms_norm_grad_workspace(int64_t M, int64_t K); /* -1 for sizes out of ra
  * tight, a byte for each block of 32), as quantize_mx4 writes them.  Else the scales
  * are NULL.  Products are exact for 8 and 4 bits, sums 32-bit floats; h is rounded to
  * `type` once.  Only the weights of experts that are named are read.
- * The workspace holds expert_layer_workspace(type, T, F, top) bytes, aligned to 16.
+ * The workspace holds expert_layer_workspace(type, T, D, F, top) bytes, aligned to 16.
  * -1 type  -2 weights  -3 out_type  -4 gated not 0 or 1  -5 T  -6 D  -7 F negative
  * -8 experts < 1  -9 top < 1  -10 X  -12 ids  -13 share  -14 W_in  -17 scale_in  -18 W_out
  * -21 scale_out  -22 Y NULL while not empty (scales: or given with weights in `type`)
@@ -90,7 +90,7 @@ int expert_layer(int32_t type, int32_t weights, int32_t out_type, int32_t gated,
                  int64_t stride_in, const void* scale_in, const void* W_out, int64_t ldw_out,
                  int64_t stride_out, const void* scale_out, void* Y, int64_t ldy, void* workspace,
                  int64_t workspace_bytes, void* stream);
-int64_t expert_layer_workspace(int32_t type, int64_t T, int64_t F, int32_t top); /* -1: out of range */
+int64_t expert_layer_workspace(int32_t type, int64_t T, int64_t D, int64_t F, int32_t top); /* -1: out of range */
 
 /* Static string for a status of these calls (never NULL). */
 const char* layer_status_string(int status);

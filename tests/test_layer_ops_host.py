@@ -140,7 +140,7 @@ def layer_call(type=1, weights=1, out=1, gated=1, T=4, D=32, F=16, E=8, top=2, X
                W_in=FAKE * 8, ldi=32, si=1024, sci=None, W_out=FAKE * 16, ldo=16, so=512, sco=None, Y=FAKE * 32, ldy=32,
                work=FAKE * 64, room=None):
     if room is None:
-        room = _lib.expert_layer_workspace(type, T, F, top)
+        room = _lib.expert_layer_workspace(type, T, D, F, top)
     return _lib.expert_layer(type, weights, out, gated, T, D, F, E, top, X, ldx, ids, share, W_in, ldi, si, sci, W_out, ldo, so,
                              sco, Y, ldy, work, room, None)
 
@@ -155,8 +155,8 @@ BLOCKS = dict(weights=5, sci=FAKE * 128, sco=FAKE * 256, ldi=16, si=512, ldo=8, 
     (dict(ids=None), -12), (dict(share=None), -13), (dict(W_in=None), -14), (dict(ldi=31), -15), (dict(si=-1), -16),
     (dict(sci=FAKE * 128), -17), (dict(SCALED, sci=None), -17), (dict(BLOCKS, ldi=15), -15), (dict(W_out=None), -18),
     (dict(ldo=15), -19), (dict(BLOCKS, ldo=7), -19), (dict(so=-1), -20), (dict(sco=FAKE * 256), -21), (dict(BLOCKS, sco=None), -21),
-    (dict(Y=None), -22), (dict(ldy=31), -23), (dict(work=None), -24), (dict(work=FAKE * 64 + 8), -24), (dict(room=255), -25),
-    (dict(T=65, room=1 << 20), 5), (dict(T=64, top=9, room=1 << 20), 5), (dict(E=4097), 5), (dict(ldi=1 << 21), 5),
+    (dict(Y=None), -22), (dict(ldy=31), -23), (dict(work=None), -24), (dict(work=FAKE * 64 + 8), -24), (dict(room=2175), -25),
+    (dict(T=65, room=1 << 20), 5), (dict(T=64, top=9, room=1 << 20), 5), (dict(E=1025), 5), (dict(ldi=1 << 21), 5),
     (dict(F=(1 << 19) + 1, ldo=1 << 20, room=1 << 40), 5), (dict(si=(1 << 40) + 1), 5),
     (dict(Y=FAKE + 2), 3), (dict(Y=FAKE * 2 + 31), 3), (dict(Y=FAKE * 4), 3), (dict(Y=FAKE * 8 + 2 * (7 * 1024 + 1023)), 3),
     (dict(Y=FAKE * 16 + 2 * (7 * 512 + 511)), 3), (dict(work=FAKE * 32), 3), (dict(work=FAKE * 8), 3), (dict(work=FAKE), 3),
@@ -167,10 +167,12 @@ def test_expert_layer_codes(change, code):
 
 
 def test_layer_workspace():
-    assert _lib.expert_layer_workspace(1, 4, 16, 2) == 4 * 2 * 32
-    assert _lib.expert_layer_workspace(0, 3, 5, 1) == 3 * 32  # rows start at multiples of 16 bytes
-    assert _lib.expert_layer_workspace(1, 65, 16, 1) == _lib.expert_layer_workspace(1, 64, 16, 9) == -1
-    assert _lib.expert_layer_workspace(3, 1, 1, 1) == _lib.expert_layer_workspace(1, 1, 1, 0) == -1
+    f = _lib.expert_layer_workspace
+    # h and products of every pair in whole lines of 128 bytes, and counters.
+    assert f(1, 4, 32, 16, 2) == 4 * 2 * (128 + 128) + 128
+    assert f(0, 3, 33, 65, 1) == 3 * (384 + 256) + 128
+    assert f(1, 0, 32, 16, 2) == f(1, 4, 0, 16, 2) == 0
+    assert f(1, 65, 8, 16, 1) == f(1, 64, 8, 16, 9) == f(3, 1, 1, 1, 1) == f(1, 1, 1, 1, 0) == f(1, 1, 1 << 20, 1, 1) == -1
 
 
 def test_status_strings():
