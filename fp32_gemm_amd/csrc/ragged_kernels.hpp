@@ -274,21 +274,32 @@ struct RaggedLoader {
   }
 };
 
-// The scales of a slice of 4-bit codes: 8 bytes of every row of A, then of B,
-// brought to LDS as they lie, 4 bytes a lane and 32 rows a load instruction,
-// which the waves that share the slice divide.  What is past the slice's last
-// block reads as 2^-127, and its codes as zero.
+// The scales of 4-bit codes: 8 bytes a slice of every row of A, then of B, brought
+// to LDS as they lie.  A load of 8 bytes of a row costs a line of 128 between the
+// caches, as much as the row's codes do, so the large tiles bring four slices'
+// scales at a time, to two places in turn (8192 x 8192 x 8192: 309 us with 8 bytes
+// at a time, 270 so); the small ones, whose waves take different slices, 8 bytes.
+// `slice` counts whole slices; the one that goes through registers is -1.
 template <class T>
 struct RaggedBlocks {
-  static constexpr int ROW = T::SL / 16;  // bytes of a row's scales
+  static constexpr int GROUP = T::WAVES_K == 1 && T::BM >= 128 ? 4 : 1;  // slices at a time
+  static constexpr int ROW = 8 * GROUP, LANE = GROUP == 4 ? 16 : 4;      // bytes of a row, and of a lane
+  static constexpr int UNIT = 32 * ROW;                                  // of a load instruction: two lanes a row
   static constexpr int UNITS_A = (T::BM + 31) / 32, UNITS_B = (T::BN + 31) / 32;
   static constexpr int NI = (UNITS_A + UNITS_B) / T::WAVES;  // load instructions a wave
-  static constexpr int AT_B = UNITS_A * 256, STAGE = (UNITS_A + UNITS_B) * 256;
-  static_assert((UNITS_A + UNITS_B) % T::WAVES == 0 && ROW == 8, "whole load instructions a wave");
-  const char* base[NI];  // of the next slice
-  int off[NI];           // this lane's bytes past it, or kRaggedMasked
+  static constexpr int PLACES = GROUP == 4 ? 2 : T::S;       // one for each stage of the ring, or two
+  static constexpr int AT_B = UNITS_A * UNIT, STAGE = (UNITS_A + UNITS_B) * UNIT;
+  static_assert((UNITS_A + UNITS_B) % T::WAVES == 0 && T::SL == 128, "whole load instructions a wave");
+  const char* base[NI];  // of slice 0
+  int off[NI];           // this lane's bytes past a slice's, or kRaggedMasked
   int first;             // the wave's first load instruction
 
+  // Four slices: the 16-byte pieces of every second eight rows change places, for
+  // the banks.
+  static __device__ __forceinline__ int piece(int row, int j) { return GROUP == 4 ? j ^ (row >> 3 & 1) : j; }
+  static __device__ __forceinline__ int place(int slice, int stage) {
+    return (GROUP == 4 ? slice >> 2 & 1 : stage) * STAGE;
+  }
   __device__ __forceinline__ void init(const unsigned char* a, const unsigned char* b, int row_bytes, int rows_a,
                                        int rows_b, int wave, int lane) {
     first = wave * NI;
@@ -298,43 +309,76 @@ struct RaggedBlocks {
       const bool of_a = u < UNITS_A;
       const int row = (of_a ? u : u - UNITS_A) * 32 + lane / 2;
       base[j] = reinterpret_cast<const char*>(of_a ? a : b);
-      off[j] = row < (of_a ? rows_a : rows_b) ? row * row_bytes + lane % 2 * 4 : kRaggedMasked;
+      off[j] = row < (of_a ? rows_a : rows_b) ? row * row_bytes + piece(row, lane % 2) * LANE : kRaggedMasked;
     }
   }
-  __device__ __forceinline__ void skip(int bytes) {
-#pragma unroll
-    for (int j = 0; j < NI; ++j) base[j] += bytes;
-  }
-  __device__ __forceinline__ void send(rlds_t stage, bool more, int step) {
+  // With slice `slice` of `whole`, sent to stage `stage`.
+  __device__ __forceinline__ void send(rlds_t scales, int stage, int slice, int whole, int lane) {
+    if constexpr (GROUP == 4) {
+      if ((slice & 3) != 0 || slice >= whole) return;
+      if (slice + 4 > whole) {  // the last few: nothing past them is read
+        finish(scales + place(slice, stage), slice, whole - slice, lane);
+        return;
+      }
+    }
 #pragma unroll
     for (int j = 0; j < NI; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ragged_rsrc(base[j], more ? kRaggedMasked : 0),
-                                               (__attribute__((address_space(3))) void*)(stage + (first + j) * 256), 4,
-                                               off[j], 0, 0, 0);
-    skip(step);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          ragged_rsrc(base[j] + slice * 8, slice < whole ? kRaggedMasked : 0),
+          (__attribute__((address_space(3))) void*)(scales + place(slice, stage) + (first + j) * UNIT), LANE, off[j], 0,
+          0, 0);
   }
-  // Of the slice `ahead` bytes on, `left` scales of which exist, through registers.
-  __device__ __forceinline__ void fetch(int (&held)[NI], int ahead, int left, int lane) const {
+  __device__ __forceinline__ void finish(rlds_t to, int slice, int n, int lane) const {
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
-      const auto r = ragged_rsrc(base[j] + ahead, kRaggedMasked);
-      held[j] = 0;
+      const auto r = ragged_rsrc(base[j] + slice * 8, kRaggedMasked);
+      const int at = off[j] == kRaggedMasked ? 0 : piece((first + j) * 32 + lane / 2, lane % 2) * 2;  // the lane's first slice
+      const ru2 lo = __builtin_amdgcn_raw_buffer_load_b64(r, at < n ? off[j] : kRaggedMasked, 0, 0),
+                hi = __builtin_amdgcn_raw_buffer_load_b64(r, at + 1 < n && off[j] != kRaggedMasked ? off[j] + 8 : kRaggedMasked, 0, 0);
+      *(__attribute__((address_space(3))) ru4*)(to + (first + j) * UNIT + lane * 16) = ru4{lo[0], lo[1], hi[0], hi[1]};
+    }
+  }
+  // The slice through registers: `left` scales of a row at slice `at`, which need not
+  // be whole; what is past them counts as 2^-127, and its codes are zero.
+  struct Held { int word[NI][2]; };
+  __device__ __forceinline__ void fetch(Held& h, int at, int left, int row_bytes, int rows_a, int rows_b, int lane) const {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool there = lane % 2 * 4 + i < left && off[j] != kRaggedMasked;
-        held[j] |= (__builtin_amdgcn_raw_buffer_load_b8(r, there ? off[j] + i : kRaggedMasked, 0, 0) & 255) << (8 * i);
+    for (int j = 0; j < NI; ++j) {
+      const int u = first + j;
+      const bool of_a = u < UNITS_A;
+      const int row = (of_a ? u : u - UNITS_A) * 32 + lane / 2;
+      const auto r = ragged_rsrc(base[j] + at * 8, kRaggedMasked);
+      // Four slices: the lane whose piece is the last, of which the slice is the
+      // second half; else the lane's own 4 bytes.
+      const bool mine = row < (of_a ? rows_a : rows_b) && (GROUP == 1 || piece(row, lane % 2) == 1);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        h.word[j][w] = 0;
+        if (GROUP == 1 && w == 1) break;
+        const int from = GROUP == 4 ? w * 4 : lane % 2 * 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          h.word[j][w] |= (__builtin_amdgcn_raw_buffer_load_b8(
+                               r, mine && from + i < left ? row * row_bytes + from + i : kRaggedMasked, 0, 0) &
+                           255) << (8 * i);
       }
     }
   }
-  __device__ __forceinline__ void put(const int (&held)[NI], rlds_t stage, int lane) const {
+  __device__ __forceinline__ void put(const Held& h, rlds_t scales, int lane) const {
 #pragma unroll
-    for (int j = 0; j < NI; ++j)
-      *(__attribute__((address_space(3))) int*)(stage + (first + j) * 256 + lane * 4) = held[j];
+    for (int j = 0; j < NI; ++j) {
+      const rlds_t to = scales + place(-1, 0) + (first + j) * UNIT + lane * LANE;
+      if constexpr (GROUP == 4) *(__attribute__((address_space(3))) ru4*)to =
+          ru4{0, 0, static_cast<unsigned>(h.word[j][0]), static_cast<unsigned>(h.word[j][1])};
+      else *(__attribute__((address_space(3))) int*)to = h.word[j][0];
+    }
   }
   // A lane's scales of a slice of one operand's block of rows, a byte for each of its pieces.
-  static __device__ __forceinline__ int word(rlds_t stage, int at, int lane) {
-    constexpr int EACH = ROW * T::MF / 64;  // bytes a lane takes
-    const rlds_t p = stage + (at + lane % T::MF) * ROW + lane / T::MF * EACH;
+  static __device__ __forceinline__ int word(rlds_t scales, int stage, int slice, int operand, int at, int lane) {
+    constexpr int EACH = 8 * T::MF / 64;  // bytes a lane takes
+    const int row = at + lane % T::MF;
+    const rlds_t p = scales + place(slice, stage) + operand + row * ROW + lane / T::MF * EACH +
+                     (GROUP == 4 ? piece(row, slice >> 1 & 1) * 16 + (slice & 1) * 8 : 0);
     if constexpr (EACH == 4) return *(__attribute__((address_space(3))) int*)p;
     else return *(__attribute__((address_space(3))) unsigned short*)p;
   }
@@ -408,8 +452,8 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
   constexpr bool M4 = ELEM == kElemM4, BIASED = ELEM == kElemI8 || M4;
   using Blocks = std::conditional_t<M4, RaggedBlocks<std::conditional_t<M4, T, RaggedTile<64, 64, 2, 2, 1, 2, 128, 32, 2>>>,
                                     RaggedBlocks<RaggedTile<64, 64, 2, 2, 1, 2, 128, 32, 2>>>;
-  constexpr int NIS = M4 ? Blocks::NI : 0;  // load instructions of a slice's scales
-  constexpr int RING = T::RING + (M4 ? Blocks::STAGE * S * T::WAVES_K : 0);
+  constexpr int NIS = M4 && Blocks::GROUP == 1 ? Blocks::NI : 0;  // load instructions of every slice's scales
+  constexpr int RING = T::RING + (M4 ? Blocks::STAGE * Blocks::PLACES * T::WAVES_K : 0);
   __shared__ __attribute__((aligned(1024))) char lds[RING > T::LDS ? RING : T::LDS];
 
   const int lane = threadIdx.x & 63;
@@ -475,17 +519,19 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
     left_a -= T::WAVES_K;
   };
   Blocks blocks;
-  const rlds_t scales = (rlds_t)lds + T::RING + kgroup * (Blocks::STAGE * S);
-  if constexpr (M4) {
-    const int row_bytes = (p.K + 15) / 16;
+  const rlds_t scales = (rlds_t)lds + T::RING + kgroup * (Blocks::STAGE * Blocks::PLACES);
+  const int row_bytes = (p.K + 15) / 16;  // of scales
+  int slice_b = skip;  // the next one that is sent
+  if constexpr (M4)
     blocks.init(p.block_a + row_c * row_bytes, p.block_b + (static_cast<long long>(group) * p.N + n0) * row_bytes,
                 row_bytes, rows, cols, wave, lane);
-    blocks.skip(skip * Blocks::ROW);
-  }
 
   auto send_b = [&](int stage) {
     lb.send(ring + stage * T::STAGE + T::BM * SL, left_b > 0);
-    if constexpr (M4) blocks.send(scales + stage * Blocks::STAGE, left_b > 0, Blocks::ROW * T::WAVES_K);
+    if constexpr (M4) {
+      blocks.send(scales, stage, slice_b, whole, lane);
+      slice_b += T::WAVES_K;
+    }
     left_b -= T::WAVES_K;
   };
 
@@ -528,14 +574,14 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
     constexpr int NIA = LoadA::NI, NIB = LoadB::NI + NIS;
     ri4 fa[2][NF], fb[2][T::FN];
     int sa_now[NF], sb_now[T::FN], sa_next[NF], sb_next[T::FN];  // 4-bit codes: the slice's scales, and the next one's
-    auto read_scales = [&](int stage) {
+    auto read_scales = [&](int stage, int slice) {
       if constexpr (M4) {
 #pragma unroll
         for (int i = 0; i < NF; ++i)
-          sa_next[i] = Blocks::word(scales + stage * Blocks::STAGE, block_row(i), lane);
+          sa_next[i] = Blocks::word(scales, stage, slice, 0, block_row(i), lane);
 #pragma unroll
         for (int j = 0; j < T::FN; ++j)
-          sb_next[j] = Blocks::word(scales + stage * Blocks::STAGE + Blocks::AT_B, bn + j * MF, lane);
+          sb_next[j] = Blocks::word(scales, stage, slice, Blocks::AT_B, bn + j * MF, lane);
       }
     };
     auto turn_scales = [&] {
@@ -574,7 +620,8 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
     };
     ragged_barrier<(S - 2) * (NIA + NIB) + NIA, ALONE>();
     read(0, ring, 0);
-    read_scales(0);
+    int slice_now = skip;  // that is multiplied
+    read_scales(0, slice_now);
     turn_scales();
     int at = 0;
     // Step group ks of the slice in stage `at` is multiplied from one half of
@@ -587,7 +634,7 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
         ragged_barrier<(S - 2) * (NIA + NIB), ALONE>();
         __builtin_amdgcn_sched_barrier(0);
         read(0, ring + (at + 1 == S ? 0 : at + 1) * T::STAGE, 0);
-        read_scales(at + 1 == S ? 0 : at + 1);
+        read_scales(at + 1 == S ? 0 : at + 1, slice_now += T::WAVES_K);
         send_a(at);
       } else {
         read(1 - half, ring + at * T::STAGE, ks + 1);
@@ -622,13 +669,13 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
   // A slice through registers: `left` steps of the reduction from step `done`.
   typename LoadA::Held ha;
   typename LoadB::Held hb;
-  int hs[NIS + !NIS] = {};
+  typename Blocks::Held hs;
   auto fetch = [&](int done, int left) {
     if constexpr (A_ALONG) la.fetch(ha, a + done * ES, done * ES, left * ES, narrow_a, lane);
     else la.fetch(ha, a + done * p.lda, m_bytes, left, narrow_a, lane);
     if constexpr (B_ALONG) lb.fetch(hb, b + done * ES, done * ES, left * ES, narrow_b, lane);
     else lb.fetch(hb, b + done * p.ldb, n0 * ES, left, narrow_b, lane);
-    if constexpr (M4) blocks.fetch(hs, done / 16 - skip * Blocks::ROW, (left + 15) / 16, lane);
+    if constexpr (M4) blocks.fetch(hs, done / SL, (left + 15) / 16, row_bytes, rows, cols, lane);
   };
   auto put = [&] {
     la.put(ha, ring, lane);
@@ -667,7 +714,7 @@ __global__ __launch_bounds__(T::NT, T::PER_SIMD) void ragged_kernel(const Ragged
       fetch(len - head, head);  // first, for its loads to come back first
       la.base += la.step;
       lb.base += lb.step;
-      if constexpr (M4) blocks.skip(Blocks::ROW * T::WAVES_K);
+      slice_b += T::WAVES_K;
       left_a -= T::WAVES_K;
       left_b -= T::WAVES_K;
     } else {
