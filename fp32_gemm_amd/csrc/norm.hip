@@ -6,7 +6,9 @@
 //   dx = s (g - n mean(g n)) + dh,  dw = sum over rows of dy n,  g = dy w, n = h s
 //
 // Sums of squares, s and the largest |v| are held in 64 bits, so that no row of
-// finite numbers overflows and codes are those of the exact quotients.
+// finite numbers overflows and codes are those of the exact quotients.  The largest
+// |v| is looked for in 32 bits first; only the 16-byte pieces that may hold it, and
+// codes next to a tie, are computed again in 64.
 #include "norm.hpp"
 
 #include "ragged_kernels.hpp"
@@ -64,12 +66,14 @@ struct Weights {
   static constexpr int WELEM = W32 ? kElemF32 : ELEM;
   Piece<WELEM> part[WORDS];
   __device__ __forceinline__ void load(const char* w, long long piece) {
-    if (w == nullptr) return;
+    constexpr int kOne = WELEM == kElemF32 ? 0x3F800000 : WELEM == kElemBF16 ? 0x3F803F80 : 0x3C003C00;
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i) part[i].load(w, piece * WORDS + i);
+    for (int i = 0; i < WORDS; ++i) part[i].raw = ri4{kOne, kOne, kOne, kOne};
+    if (w != nullptr)
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) part[i].load(w, piece * WORDS + i);
   }
-  __device__ __forceinline__ float at(const char* w, int i) const {
-    if (w == nullptr) return 1.0f;
+  __device__ __forceinline__ float at(int i) const {
     if constexpr (W32) return part[i / 4][i % 4];
     else return part[0][i];
   }
@@ -142,24 +146,30 @@ __device__ __forceinline__ double inverse_root(double m) {
   return m == 0.0 || m == __builtin_inf() ? y : y * __builtin_fma(-0.5 * m * y, y, 1.5);
 }
 
-// A code decided in 32 bits is off by at most 127 * 6 * 2^-24 before it is
-// rounded (h, v, the largest |v|, its inverse and the product round once each), so
-// values that near a tie, and rows whose inverse might leave the range, are
-// divided in 64 bits.
-constexpr float kNearTie = 0x1p-13f;
+// A code decided in 32 bits is off by at most 127 * 5 * 2^-24 < 2^-14 before it is
+// rounded (h, v, the largest |v|, its inverse and the product round once each).
+// Values that near a tie, and rows whose inverse might leave the range, are multiplied
+// in 64 bits, which is off by less than 2^-43, and those that are nearer than kTie
+// even then are divided.
+constexpr float kNearTie = 0x1p-14f;
+constexpr double kTie = 0x1p-40;
 
 constexpr int kNormBlocks = 1 << 23;  // workgroups in x; more rows go on in y
 
 // One row by THREADS threads of 256, KEEP pieces a thread in registers as they
 // came; longer rows are read again.  H may be x or r itself: a thread has read
 // what it overwrites, and where rows are read twice, H is written the second time.
+// Memory-bound without codes: bf16 8192 x 8192 with a residual 102 us, 5.3 TB/s, as a
+// copy runs.  With codes as well bound by the two reductions' latencies: 103 us for
+// 7 bytes a value, 4.6 TB/s (weights read again for the codes: 114; the largest |v|
+// in 64 bits throughout, and a division for every value near a tie: 116).
 template <int ELEM, bool W32, int THREADS, int KEEP, bool CODES>
 __global__ __launch_bounds__(256) void rms_norm_kernel(const NormArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
   using P = Piece<ELEM>;
   using W = Weights<ELEM, W32>;
   constexpr int ES = elem_size(ELEM), PER = P::PER;
-  __shared__ double room[4][2];
+  __shared__ double room[2][4][2];
   const int in = threadIdx.x % THREADS;
   const long long block = static_cast<long long>(blockIdx.y) * kNormBlocks + blockIdx.x;
   const long long row = block * (256 / THREADS) + threadIdx.x / THREADS;
@@ -171,6 +181,7 @@ __global__ __launch_bounds__(256) void rms_norm_kernel(const NormArgs p) {
   const bool one = in < rest;
 
   P kx[KEEP], kr[KEEP];
+  W kw[CODES ? KEEP : 1];  // both passes of codes need them
 #pragma unroll
   for (int j = 0; j < KEEP; ++j) {
     const int c = in + j * THREADS;
@@ -180,39 +191,85 @@ __global__ __launch_bounds__(256) void rms_norm_kernel(const NormArgs p) {
       if (r) kr[j].load(r, c);
     }
   }
+  if constexpr (CODES)
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j)
+      if (in + j * THREADS < pieces) kw[j].load(p.w, in + j * THREADS);
   const float x1 = one ? element<ELEM>(x, last) : 0.0f, r1 = one && r ? element<ELEM>(r, last) : 0.0f;
-  double sum = 0, top = 0, bad = 0;
-  auto take = [&](float a, float b, float w) {
-    const double h = static_cast<double>(a) + static_cast<double>(b);
-    sum = __builtin_fma(h, h, sum);
+  double sum = 0;
+  // In 32 bits: the largest |v| of each piece that is kept, of the others, and NaN
+  // once a value is not finite.
+  float most[KEEP], most_rest = 0.0f, bad = 0.0f;
+  auto take = [&](float a, float b, float w, float& largest) {
+    const float h = a + b;
+    const double d = h;
+    sum = __builtin_fma(d, d, sum);
     if constexpr (CODES) {
-      const double v = h * static_cast<double>(w);
-      top = __builtin_fmax(top, __builtin_fabs(v));
-      bad = __builtin_fma(v, 0.0, bad);  // NaN once a value is not finite
+      const float v = h * w;
+      largest = __builtin_fmaxf(largest, __builtin_fabsf(v));
+      bad = __builtin_fmaf(v, 0.0f, bad);
     }
   };
-  auto take_piece = [&](const P& a, const P& b, int c) {
-    W w;
-    if constexpr (CODES) w.load(p.w, c);
+  auto take_piece = [&](const P& a, const P& b, const W& w, float& largest) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) take(a[i], b[i], CODES ? w.at(p.w, i) : 1.0f);
+    for (int i = 0; i < PER; ++i) take(a[i], b[i], CODES ? w.at(i) : 1.0f, largest);
+  };
+  // Calls with each piece past the kept ones, which is read again.
+  auto others = [&](auto with) {
+    for (int c = in + KEEP * THREADS; c < pieces; c += THREADS) {
+      P a, b;
+      a.load(x, c);
+      b.raw = ri4{};
+      if (r) b.load(r, c);
+      W w;
+      w.load(p.w, c);
+      with(a, b, w, c);
+    }
   };
 #pragma unroll
   for (int j = 0; j < KEEP; ++j) {
+    most[j] = 0.0f;
     const int c = in + j * THREADS;
-    if (c < pieces) take_piece(kx[j], kr[j], c);
+    if (c < pieces) take_piece(kx[j], kr[j], kw[CODES ? j : 0], most[j]);
   }
-  if (one) take(x1, r1, CODES ? W::one(p.w, last) : 1.0f);
-  for (int c = in + KEEP * THREADS; c < pieces; c += THREADS) {
-    P a, b;
-    a.load(x, c);
-    b.raw = ri4{};
-    if (r) b.load(r, c);
-    take_piece(a, b, c);
+  if (one) take(x1, r1, CODES ? W::one(p.w, last) : 1.0f, most_rest);
+  others([&](const P& a, const P& b, const W& w, int) { take_piece(a, b, w, most_rest); });
+  double top = 0;
+  if constexpr (CODES) {
+    float largest = most_rest;
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j) largest = __builtin_fmaxf(largest, most[j]);
+    top = bad == 0.0f ? largest : __builtin_inff();
   }
-  if constexpr (CODES)
-    if (bad != 0.0) top = __builtin_inf();
-  over_row<Add, Larger, THREADS>(sum, top, room);
+  over_row<Add, Larger, THREADS>(sum, top, room[0]);
+  if constexpr (CODES) {
+    // |v| in 32 bits is off by at most 2 * 2^-24 of itself, so the largest lies within
+    // 2^-21 of the largest found.  Where that is tiny or no number, all are looked at.
+    const double from = top > 0x1p-100 && top < __builtin_inf() ? top * (1.0 - 0x1p-21) : -1.0;
+    double exact = 0, wrong = 0;
+    auto look = [&](float a, float b, float w) {
+      const double v = (static_cast<double>(a) + static_cast<double>(b)) * static_cast<double>(w);
+      exact = __builtin_fmax(exact, __builtin_fabs(v));
+      wrong = __builtin_fma(v, 0.0, wrong);
+    };
+    auto look_piece = [&](const P& a, const P& b, const W& w, int) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) look(a[i], b[i], w.at(i));
+    };
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j) {
+      const int c = in + j * THREADS;
+      if (c < pieces && most[j] >= from) look_piece(kx[j], kr[j], kw[j], c);
+    }
+    if (most_rest >= from) {
+      if (one) look(x1, r1, W::one(p.w, last));
+      others(look_piece);
+    }
+    if (wrong != 0.0) exact = __builtin_inf();
+    double none = 0;
+    over_row<Add, Larger, THREADS>(none, exact, room[1]);
+    top = exact;
+  }
   const double s = inverse_root(__builtin_fma(sum, p.inv_k, static_cast<double>(p.eps)));
   // s in 32 bits, with a power of two of its own where it would leave their range.
   const float before = s < 0x1p-100 ? 0x1p-64f : s > 0x1p100 ? 0x1p64f : 1.0f;
@@ -227,40 +284,51 @@ __global__ __launch_bounds__(256) void rms_norm_kernel(const NormArgs p) {
   char* const h = p.h ? p.h + row * p.ldh * ES : nullptr;
   char* const y = p.y ? p.y + row * p.ldy * (p.out32 ? 4 : ES) : nullptr;
   signed char* const q = CODES ? p.q + row * p.ldq : nullptr;
+  // The inverse's estimate, after two steps of Newton's method.
+  double inv64 = CODES ? __builtin_amdgcn_rcp(top) : 0.0;
+  if constexpr (CODES) {
+    inv64 = __builtin_fma(inv64, __builtin_fma(-top, inv64, 1.0), inv64);
+    inv64 = __builtin_fma(inv64, __builtin_fma(-top, inv64, 1.0), inv64) * 127.0;
+  }
   auto code64 = [&](float a, float b, float w) {
     const double v = (static_cast<double>(a) + static_cast<double>(b)) * static_cast<double>(w);
-    return usable ? static_cast<int>(__builtin_rint(v * 127.0 / top)) : 0;
+    double t = v * inv64;
+    // (A tiny or huge `top` has no finite estimate: then t is no number near a tie's
+    // distance, and is divided.)
+    const double off = __builtin_fabs(t - __builtin_rint(t));
+    if (!(off < 0.5 - kTie)) t = v * 127.0 / top;
+    return usable ? static_cast<int>(__builtin_rint(t)) : 0;
   };
-  auto write = [&](const P& a, const P& b, int c) {
-    W w;
-    w.load(p.w, c);
+  auto write = [&](const P& a, const P& b, const W& w, int c) {
     float hv[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) hv[i] = a[i] + b[i];
     if (h) P::store(h, c, hv);
     if constexpr (CODES) {
-      int code[PER];
-      bool near = in_64;
+      // t + kSnap is t rounded to an integer, in the low bits of the sum.
+      constexpr float kSnap = 1.5f * (1 << 23);
+      unsigned code[PER];
+      float off = in_64 ? 1.0f : 0.0f;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const float t = hv[i] * w.at(p.w, i) * inv, n = __builtin_rintf(t);
-        near |= __builtin_fabsf(__builtin_fabsf(t - n) - 0.5f) < kNearTie;
-        code[i] = static_cast<int>(n);
+        const float t = hv[i] * w.at(i) * inv, n = t + kSnap;
+        off = __builtin_fmaxf(off, __builtin_fabsf(t - (n - kSnap)));
+        code[i] = __builtin_bit_cast(unsigned, n);
       }
-      if (near)
+      if (off > 0.5f - kNearTie)
 #pragma unroll
-        for (int i = 0; i < PER; ++i) code[i] = code64(a[i], b[i], w.at(p.w, i));
+        for (int i = 0; i < PER; ++i) code[i] = static_cast<unsigned>(code64(a[i], b[i], w.at(i)));
       unsigned o[PER / 4];
 #pragma unroll
-      for (int i = 0; i < PER / 4; ++i)
-        o[i] = (code[4 * i] & 255u) | (code[4 * i + 1] & 255u) << 8 | (code[4 * i + 2] & 255u) << 16 |
-               static_cast<unsigned>(code[4 * i + 3]) << 24;
+      for (int i = 0; i < PER / 4; ++i)  // the low bytes of four
+        o[i] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(code[4 * i + 3], code[4 * i + 2], 0x0C0C0400u),
+                                     __builtin_amdgcn_perm(code[4 * i + 1], code[4 * i], 0x0C0C0400u), 0x05040100u);
       __builtin_memcpy(q + static_cast<long long>(c) * PER, o, PER);
     }
     if (y) {
       float v[PER];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) v[i] = hv[i] * before * s32 * w.at(p.w, i);
+      for (int i = 0; i < PER; ++i) v[i] = hv[i] * before * s32 * w.at(i);
       if (ELEM != kElemF32 && p.out32) __builtin_memcpy(y + static_cast<long long>(c) * PER * 4, v, PER * 4);
       else P::store(y, c, v);
     }
@@ -268,7 +336,10 @@ __global__ __launch_bounds__(256) void rms_norm_kernel(const NormArgs p) {
 #pragma unroll
   for (int j = 0; j < KEEP; ++j) {
     const int c = in + j * THREADS;
-    if (c < pieces) write(kx[j], kr[j], c);
+    if (c < pieces) {
+      if constexpr (!CODES) kw[0].load(p.w, c);
+      write(kx[j], kr[j], kw[CODES ? j : 0], c);
+    }
   }
   if (one) {
     const float hv = x1 + r1, w = W::one(p.w, last);
@@ -280,19 +351,14 @@ __global__ __launch_bounds__(256) void rms_norm_kernel(const NormArgs p) {
       else set_element<ELEM>(y, last, v);
     }
   }
-  for (int c = in + KEEP * THREADS; c < pieces; c += THREADS) {
-    P a, b;
-    a.load(x, c);
-    b.raw = ri4{};
-    if (r) b.load(r, c);
-    write(a, b, c);
-  }
+  others(write);
 #endif
 }
 
 // The gradient: a team of THREADS threads takes every teams-th row, with its sums
 // for dw in registers, P pieces a thread (0: any length, the sums in memory), and
-// leaves them as a row of `partial`.
+// leaves them as a row of `partial`.  Memory-bound: bf16 16384 x 4096 with dh 111 us,
+// 4.9 TB/s, and 5.5 us for the teams' sums.
 template <int ELEM, bool W32, int THREADS, int PIECES>
 __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_grad_kernel(const NormGradArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
@@ -343,7 +409,7 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_grad_k
       for (int j = 0; j < HELD; ++j)
         if (in + j * THREADS < pieces)
 #pragma unroll
-          for (int i = 0; i < PER; ++i) take(kh[j][i], kd[j][i], w[j].at(p.w, i));
+          for (int i = 0; i < PER; ++i) take(kh[j][i], kd[j][i], w[j].at(i));
     } else {
       for (int c = in; c < pieces; c += THREADS) {
         P a, b;
@@ -351,7 +417,7 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_grad_k
         b.load(dy, c);
         w[0].load(p.w, c);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) take(a[i], b[i], w[0].at(p.w, i));
+        for (int i = 0; i < PER; ++i) take(a[i], b[i], w[0].at(i));
       }
     }
     const float h1 = one ? element<ELEM>(h, last) : 0.0f, d1 = one ? element<ELEM>(dy, last) : 0.0f;
@@ -368,7 +434,7 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_grad_k
     auto piece = [&](const P& a, const P& b, const P& r, const W& wv, int c, float (&sums)[PER]) {
       float v[PER];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) v[i] = grad(a[i], b[i], r[i], wv.at(p.w, i), sums[i]);
+      for (int i = 0; i < PER; ++i) v[i] = grad(a[i], b[i], r[i], wv.at(i), sums[i]);
       P::store(dx, c, v);
     };
     if constexpr (PIECES) {
@@ -404,7 +470,7 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_grad_k
 #endif
 }
 
-// dw: the teams' sums, a column by four threads that take every 4th team, in a
+// dw: the teams' sums, a column by sixteen threads that take every 16th team, in a
 // fixed order.
 constexpr int kSumColumns = 64, kSumGroups = 16;
 template <int OUT>
@@ -436,10 +502,12 @@ const void* norm_kernel(bool codes) {
 
 template <int ELEM, bool W32>
 hipError_t launch_norm(const NormArgs& args, hipStream_t s) {
-  // A wave takes rows of up to two pieces a lane, and of up to eight where there
-  // are rows enough for all waves; longer ones go to four waves.
+  // A wave takes rows of up to two pieces a lane, and where there are rows enough for
+  // all waves of up to eight, or four with codes (16384 x 4096, residual and codes:
+  // 111 us with eight, 96 by four waves); longer ones go to four waves.
   const int pieces = args.K / Piece<ELEM>::PER;
-  const bool wave = pieces <= 128 || (pieces <= 512 && args.M >= 4096), codes = args.scale != nullptr;
+  const bool codes = args.scale != nullptr;
+  const bool wave = pieces <= 128 || (pieces <= (codes ? 256 : 512) && args.M >= 4096);
   const int each = wave ? (pieces + 63) / 64 : (pieces + 255) / 256;
   const void* const kernel = wave ? (each <= 1   ? norm_kernel<ELEM, W32, 64, 1>(codes)
                                      : each <= 2 ? norm_kernel<ELEM, W32, 64, 2>(codes)

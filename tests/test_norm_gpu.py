@@ -1,8 +1,10 @@
 """The norm, its 8-bit output and its gradient on the GPU against 64 bits.
 
-Y = H * s * weight: the sum, s, and two products round once each in 32 bits, so Y is
-off by at most 5 * 2^-24 of itself, and half a step of its type.  The scale is made in
-64 bits and rounded once.  Codes must be those of the quotients in 64 bits.
+H rounds once in 32 bits, so its squares are off by 2 * 2^-24 and s by half of that.
+Y = H * s * weight: H, what s has from it, s itself and two products round, so Y is off
+by at most 5 * 2^-24 of itself, and half a step of its type.  The scale is made in 64
+bits from the exact largest value and s, and rounded once: 2 * 2^-24.  Codes must be
+those of the quotients in 64 bits.
 """
 import pytest
 import torch
@@ -53,7 +55,7 @@ def check(x, r, w, eps, y=None, h=None, q=None, scale=None):
     if q is not None:
         code, sc = codes_of(v, s)
         assert torch.equal(q, code)
-        assert ((scale.double() - sc).abs() <= sc.abs() * (2.0 ** -24 + 2.0 ** -40)).all()
+        assert ((scale.double() - sc).abs() <= sc.abs() * (2 * 2.0 ** -24 + 2.0 ** -40)).all()
 
 
 SIZES = [(1, 1), (1, 7), (3, 64), (5, 100), (2, 511), (4, 512), (9, 1031), (6, 2048), (3, 4097), (2, 8192), (1, 16384), (2, 16390),
@@ -160,7 +162,7 @@ def test_extremes(K):
         assert ((y[rows].double() - want).abs() <= want.abs() * 6 * 2.0 ** -24 * 1.01 + 2.0 ** -149).all()
         code, sc = codes_of(v, s)
         assert torch.equal(q, torch.where(torch.isfinite(scale)[:, None], code, q))
-        assert ((scale[rows].double() - sc[rows]).abs() <= sc[rows].abs() * (2.0 ** -24 + 2.0 ** -40) + 2.0 ** -150).all()
+        assert ((scale[rows].double() - sc[rows]).abs() <= sc[rows].abs() * (2 * 2.0 ** -24 + 2.0 ** -40) + 2.0 ** -150).all()
         if eps:
             assert (q[3] == 0).all() and scale[3] == 0 and (y[3] == 0).all()
 
