@@ -36,20 +36,22 @@ def make_weights(g, kind, E, rows, depth, dtype):
     return q, s, unpack(q, s)[..., :depth]
 
 
-def reference(x, ids, share, w_in, w_out, gated, held, scaled):
+def reference(x, ids, share, w_in, w_out, gated, held, scaled, terms=None):
     """y in 64 bits, and how far a result may be off before its own rounding; `held`:
-    the type of h, `scaled`: whether sums are scaled afterwards."""
+    the type of h, `scaled`: whether sums are scaled afterwards, `terms`: how many
+    products of either sum are not zero (adding zero rounds nothing), if not all."""
     x, share = x.double(), share.double()
     y, off = torch.zeros_like(x), torch.zeros_like(x)
     step = 2.0 ** -24
-    D, F = w_in.shape[2], w_out.shape[2]
+    F = w_out.shape[2]
+    deep, wide = terms or (w_in.shape[2], F)
     for t in range(x.shape[0]):
         for j in range(ids.shape[1]):
             e = int(ids[t, j])
             if not 0 <= e < w_in.shape[0]:
                 continue
             u = w_in[e] @ x[t]
-            du = (2 * (D + 4) + 2 * scaled) * step * (w_in[e].abs() @ x[t].abs())
+            du = (2 * (deep + 4) + 2 * scaled) * step * (w_in[e].abs() @ x[t].abs())
             a, da = (u[:F], du[:F]) if gated else (u, du)
             h = a * torch.sigmoid(a)
             dh = 1.1 * da + 8 * step * h.abs()  # silu's slope stays below 1.1; exponential, sum and quotient
@@ -60,7 +62,7 @@ def reference(x, ids, share, w_in, w_out, gated, held, scaled):
             dh = dh + HALF_STEP[held] * (h.abs() + dh) + TINY[held]
             y[t] += share[t, j] * (w_out[e] @ h)
             # The sum over F, its scale and share, and the sum over waves and experts.
-            off[t] += share[t, j].abs() * (w_out[e].abs() @ dh + (2 * (F + 4) + 2 * scaled + 24) * step * (w_out[e].abs() @ (h.abs() + dh)))
+            off[t] += share[t, j].abs() * (w_out[e].abs() @ dh + (2 * (wide + 4) + 2 * scaled + 24) * step * (w_out[e].abs() @ (h.abs() + dh)))
     return y, off
 
 
@@ -87,6 +89,9 @@ SHAPES = [  # experts, tokens, choices, D, F
     (1, 1, 1, 1, 1), (2, 1, 1, 7, 5), (4, 1, 2, 64, 64), (8, 1, 2, 512, 256), (6, 5, 2, 129, 77), (3, 16, 3, 100, 33),
     (8, 17, 2, 256, 128), (5, 33, 2, 96, 160), (2, 64, 2, 130, 70), (16, 64, 8, 65, 31), (300, 20, 4, 48, 40),
     (4, 2, 2, 2100, 1100), (3, 40, 1, 1030, 516), (1, 64, 1, 520, 264),
+    (2, 3, 2, 4500, 300), (2, 20, 2, 300, 4500),        # reductions whose values do not stay in registers
+    (16, 16, 4, 2048, 256), (32, 16, 4, 500, 1030), (32, 12, 4, 2100, 130),  # several sets of rows a workgroup
+    (40, 10, 8, 64, 96), (90, 60, 2, 40, 64), (1024, 30, 3, 33, 20),         # many experts
 ]
 
 
@@ -199,3 +204,34 @@ def test_nothing_to_multiply():
     fg.expert_layer(e(3, 8), ids, share, e(2, 0, 8), e(2, 8, 0), y)
     assert (y == 0).all()
     fg.expert_layer(e(0, 8), ids[:0], share[:0], e(2, 4, 8), e(2, 8, 2), e(0, 8))
+
+
+@pytest.mark.parametrize("dtype,kind", [(F32, "same"), (BF16, "same"), (F16, "same"), (F32, "int8"), (BF16, "int8"), (F16, "int8"),
+                                        (F32, "mx4"), (BF16, "mx4"), (F16, "mx4")])
+@pytest.mark.parametrize("E,T,top,D,F", [(3, 1, 2, 517, 291), (5, 7, 2, 1030, 700), (4, 30, 3, 333, 1100), (2, 4, 1, 4610, 64),
+                                         (2, 21, 2, 64, 4610), (32, 16, 4, 300, 1030)])
+def test_every_place_counts_once(dtype, kind, E, T, top, D, F):
+    # A handful of values and columns that are not zero, anywhere, the first and last
+    # among them: sums of few terms leave little room for a piece lost or taken twice.
+    g = gen(D + F)
+    few = 6
+    w_in, s_in, v_in = make_weights(g, kind, E, 2 * F, D, dtype)
+    w_out, s_out, v_out = make_weights(g, kind, E, D, F, dtype)
+    x = torch.zeros(T, D, device="cuda", dtype=dtype)
+    for t in range(T):
+        at = torch.cat([torch.tensor([0, D - 1], device="cuda"), torch.randint(0, D, (few - 2,), device="cuda", generator=g)])
+        x[t, at] = torch.randn(few, device="cuda", generator=g).to(dtype)
+    keep = torch.zeros(F, dtype=torch.bool, device="cuda")
+    keep[torch.cat([torch.tensor([0, F - 1], device="cuda"), torch.randint(0, F, (few - 2,), device="cuda", generator=g)])] = True
+    v_out = torch.where(keep, v_out, 0.0)
+    if kind == "mx4":
+        pairs = torch.nn.functional.pad(keep, (0, F % 2)).view(-1, 2)
+        w_out &= (pairs[:, 0] * 15 + pairs[:, 1] * 240).to(torch.uint8)
+    else:
+        w_out[..., ~keep] = 0
+    ids = torch.stack([torch.randperm(E, device="cuda", generator=g)[:top] for _ in range(T)]).to(torch.int32)
+    share = torch.rand(T, top, device="cuda", generator=g)
+    y = torch.empty(T, D, device="cuda")  # 32 bits: nothing is lost at the end
+    fg.expert_layer(x, ids, share, w_in, w_out, y, s_in, s_out)
+    want, off = reference(x, ids, share, v_in, v_out, True, dtype, kind == "int8", terms=(few, few))
+    assert ((y.double() - want).abs() <= off * (1 + 2.0 ** -20) + 2.0 ** -24 * want.abs() + TINY[F32]).all()
