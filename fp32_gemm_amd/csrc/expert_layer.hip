@@ -286,7 +286,7 @@ struct Rows {
   using Fm = Format<XE, WE>;
   static constexpr bool KEPT = Q > 0;
   static constexpr int XT = KEPT ? Q : 1;
-  static constexpr bool AHEAD = KEPT || U * (NB * 4 + Fm::XV * 4) <= 48;  // as far as registers go
+  static constexpr bool AHEAD = KEPT || U * (NB * 4 + Fm::XV * 4) <= (NB == 1 ? 64 : 48);  // as far as registers go
   struct Held {
     ri4 w[U][NB];
     int s[U][NB];  // 4-bit codes: the blocks' scales, as loaded
@@ -410,7 +410,33 @@ struct Rows {
       }
   }
   // What whole steps of 64 bytes leave of the rows: nothing past them is read, and
-  // what is missing counts as zero.
+  // what is missing counts as zero.  Where weights and values have one type and rows
+  // are 16 bytes or more, the 16 bytes that end with them are loaded with the block's
+  // first turn and shifted down; else all of it waits for the turns.
+  struct Rest {
+    ri4 w[NB], x;
+  };
+  __device__ __forceinline__ bool ahead_of_rest() const { return Fm::SAME && row_bytes >= 16; }
+  __device__ __forceinline__ void load_rest(Rest& h, int block) const {
+    const int at = full * 64 + lane / 16 * 16, n = row_bytes - at, back = n > 0 && n < 16 ? 16 - n : 0;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int row = clamped(row_of(block, b));
+      h.w[b] = __builtin_bit_cast(
+          ri4, __builtin_amdgcn_raw_buffer_load_b128(ragged_rsrc(rows[b] + row * ld, kRaggedMasked),
+                                                     n > 0 ? lane_row(row) * static_cast<int>(ld) + at - back : kRaggedMasked, 0, 0));
+    }
+    h.x = __builtin_bit_cast(
+        ri4, __builtin_amdgcn_raw_buffer_load_b128(ragged_rsrc(values, kRaggedMasked),
+                                                   n > 0 && x_off != kRaggedMasked ? x_off + at - back : kRaggedMasked, 0, 0));
+  }
+  __device__ __forceinline__ void multiply_rest(rf4 (&acc)[NB], const Rest& h) const {
+    const int n = row_bytes - (full * 64 + lane / 16 * 16), back = n > 0 && n < 16 ? 16 - n : 0;
+    auto down = [&](const ri4& v) { return __builtin_bit_cast(ri4, __builtin_bit_cast(unsigned __int128, v) >> (8 * back)); };
+    const ri4 x = down(h.x);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) ragged_mma<XE, 16>(acc[b], down(h.w[b]), x);
+  }
   __device__ __forceinline__ void multiply_tail(rf4 (&acc)[NB], int block) const {
     const int at = full * 64 + lane / 16 * 16, n = row_bytes - at;  // valid bytes from here
     ri4 w[NB];
@@ -475,8 +501,20 @@ struct Rows {
   __device__ __forceinline__ void run(int lo, int hi, Held& a, F end) {
     rf4 acc[NB] = {};
     Held b;
+    Rest rest;
+    auto begin = [&](int block) {
+      if constexpr (Fm::SAME)
+        if (tail && ahead_of_rest()) load_rest(rest, block);
+    };
     auto done = [&](int block) {
-      if (tail) multiply_tail(acc, block);
+      if (tail) {
+        if constexpr (Fm::SAME) {
+          if (ahead_of_rest()) multiply_rest(acc, rest);
+          else multiply_tail(acc, block);
+        } else {
+          multiply_tail(acc, block);
+        }
+      }
       end(block, acc);
 #pragma unroll
       for (int i = 0; i < NB; ++i) acc[i] = rf4{};
@@ -490,6 +528,7 @@ struct Rows {
         for (int i = 0; i < BLOCKS * Q; ++i) {
           const int now = block + i / Q, next = block + (i + 1) / Q;
           if (now < hi) {
+            if (i % Q == 0) begin(now);
             if (next < hi) load(i % 2 ? a : b, next, (i + 1) % Q);
             multiply(acc, i % 2 ? b : a, i % Q);
             if (i % Q == Q - 1) done(now);
@@ -499,6 +538,7 @@ struct Rows {
     } else {
       for (int block = lo; block < hi; ++block) {
         int turn = 0;
+        begin(block);
         if constexpr (AHEAD) {
           if (block > lo) load(a, block, 0);
           for (; turn + 2 < turns; turn += 2) {
@@ -822,19 +862,19 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) 
 // (one token, 2 of 16 experts, bf16, 4096 by 2048: the layer takes 28 us so, 33 with
 // the kernel above); with more experts than waves each wave has too many short
 // pieces (8 tokens, 2 choices of 32: 24 us and 19).
-constexpr int kDirectPairs = 8;
+constexpr int kDirectTokens = 16, kDirectExperts = kWaves;
 template <int XE, int WE>
 __global__ __launch_bounds__(kThreads, 2) void expert_out_kernel(const LayerArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
   using Fm = Format<XE, WE>;
   constexpr int STEP_REGS = 4 + 4 * Fm::XV, U = STEP_REGS <= 8 ? 8 : STEP_REGS <= 16 ? 4 : STEP_REGS <= 24 ? 2 : 1;
   using R = Rows<XE, WE, U, 0, 1>;
-  __shared__ float sums[kWaves][kDirectPairs][kRows + 1];
+  __shared__ float sums[kWaves][kDirectTokens][kRows + 1];
   __shared__ short lists[kWaves][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   FewPairs few;
   few.init(p, lane);
-  for (int i = lane; i < kDirectPairs * (kRows + 1); i += 64) (&sums[wave][0][0])[i] = 0.0f;
+  for (int i = lane; i < kDirectTokens * (kRows + 1); i += 64) (&sums[wave][0][0])[i] = 0.0f;
   short* const list = lists[wave];
   const int entries = __builtin_amdgcn_readfirstlane(few.entries());
   const int block = blockIdx.x, scale_blocks = (p.F + 31) / 32;
@@ -846,7 +886,7 @@ __global__ __launch_bounds__(kThreads, 2) void expert_out_kernel(const LayerArgs
     int e = 0, set = 0;
     few.entry(v, e, set);
     e = __builtin_amdgcn_readfirstlane(e);
-    const int n = __builtin_amdgcn_readfirstlane(few.list_pairs(e, 0, list, lane));
+    const int n = __builtin_amdgcn_readfirstlane(few.list_pairs(e, 16 * set, list, lane));
     const int pair = list[lane % 16 < n ? lane % 16 : 0], token = pair / p.top;
     float share = 0.0f;  // of all the token's choices of e
     for (int j = token * p.top; j < (token + 1) * p.top; ++j) share += p.ids[j] == e ? p.share[j] : 0.0f;
@@ -916,7 +956,7 @@ hipError_t launch_tokens(const LayerArgs& args, hipStream_t s) {
   const hipError_t err = hipLaunchKernel(reinterpret_cast<const void*>(&expert_kernel<XE, WE, true>), dim3(kGroups),
                                          dim3(kThreads), values, 0, s);
   if (err != hipSuccess) return err;
-  if (pairs <= kDirectPairs)
+  if (a.few && a.T <= kDirectTokens && slots <= kDirectExperts)
     return hipLaunchKernel(reinterpret_cast<const void*>(&expert_out_kernel<XE, WE>),
                            dim3((static_cast<unsigned>(a.D) + kRows - 1) / kRows), dim3(kThreads), values, 0, s);
   return hipLaunchKernel(reinterpret_cast<const void*>(&expert_kernel<XE, WE, false>), dim3(kGroups), dim3(kThreads),
