@@ -100,7 +100,7 @@ int rms_norm(int32_t type, int32_t weight_type, int32_t out_type, int64_t M, int
   a.ldy = ldy;
   a.ldq = ldq;
   a.inv_k = K > 0 ? 1.0 / static_cast<double>(K) : 0.0;
-  a.eps = eps;
+  a.eps = K > 0 ? eps : 1.0f;  // empty rows: scale 0, whatever eps
   a.M = static_cast<int>(M);
   a.K = static_cast<int>(K);
   a.out32 = out_type == GEMM_F32;

@@ -146,6 +146,15 @@ __device__ __forceinline__ double inverse_root(double m) {
   return m == 0.0 || m == __builtin_inf() ? y : y * __builtin_fma(-0.5 * m * y, y, 1.5);
 }
 
+// s in 32 bits, with a power of two of its own where it would leave their range; what
+// is multiplied by it is multiplied by `before`, exactly, first.
+struct Factor {
+  float before, value;
+  explicit __device__ __forceinline__ Factor(double s)
+      : before(s < 0x1p-100 ? 0x1p-64f : s > 0x1p100 ? 0x1p64f : 1.0f),
+        value(static_cast<float>(s < 0x1p-100 ? s * 0x1p64 : s > 0x1p100 ? s * 0x1p-64 : s)) {}
+};
+
 // A code decided in 32 bits is off by at most 127 * 5 * 2^-24 < 2^-14 before it is
 // rounded (h, v, the largest |v|, its inverse and the product round once each).
 // Values that near a tie, and rows whose inverse might leave the range, are multiplied
@@ -271,9 +280,7 @@ __global__ __launch_bounds__(256) void rms_norm_kernel(const NormArgs p) {
     top = exact;
   }
   const double s = inverse_root(__builtin_fma(sum, p.inv_k, static_cast<double>(p.eps)));
-  // s in 32 bits, with a power of two of its own where it would leave their range.
-  const float before = s < 0x1p-100 ? 0x1p-64f : s > 0x1p100 ? 0x1p64f : 1.0f;
-  const float s32 = static_cast<float>(s < 0x1p-100 ? s * 0x1p64 : s > 0x1p100 ? s * 0x1p-64 : s);
+  const Factor s32(s);
   const bool usable = top > 0.0 && top < __builtin_inf();
   const bool in_64 = !(top > 0x1p-100 && top < 0x1p100);
   const float inv = in_64 ? 0.0f : 127.0f / static_cast<float>(top);
@@ -328,7 +335,7 @@ __global__ __launch_bounds__(256) void rms_norm_kernel(const NormArgs p) {
     if (y) {
       float v[PER];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) v[i] = hv[i] * before * s32 * w.at(i);
+      for (int i = 0; i < PER; ++i) v[i] = hv[i] * s32.before * s32.value * w.at(i);
       if (ELEM != kElemF32 && p.out32) __builtin_memcpy(y + static_cast<long long>(c) * PER * 4, v, PER * 4);
       else P::store(y, c, v);
     }
@@ -346,7 +353,7 @@ __global__ __launch_bounds__(256) void rms_norm_kernel(const NormArgs p) {
     if (h) set_element<ELEM>(h, last, hv);
     if constexpr (CODES) q[last] = static_cast<signed char>(code64(x1, r1, w));
     if (y) {
-      const float v = hv * before * s32 * w;
+      const float v = hv * s32.before * s32.value * w;
       if (ELEM != kElemF32 && p.out32) reinterpret_cast<float*>(y)[last] = v;
       else set_element<ELEM>(y, last, v);
     }
@@ -425,11 +432,12 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_grad_k
     if (one) take(h1, d1, w1);
     over_row<Add, Add, THREADS>(square, dot, room[turn]);
     const double s64 = inverse_root(__builtin_fma(square, p.inv_k, static_cast<double>(p.eps)));
-    const float s = static_cast<float>(s64), mean = static_cast<float>(dot * p.inv_k * s64);
+    const Factor s(s64);
+    const float mean = static_cast<float>(dot * p.inv_k * s64);
     auto grad = [&](float a, float b, float r, float wv, float& sums) {
-      const float n = a * s;
+      const float n = a * s.before * s.value;
       sums = __builtin_fmaf(b, n, sums);
-      return __builtin_fmaf(s, __builtin_fmaf(-n, mean, b * wv), r);
+      return __builtin_fmaf(__builtin_fmaf(-n, mean, b * wv) * s.before, s.value, r);
     };
     auto piece = [&](const P& a, const P& b, const P& r, const W& wv, int c, float (&sums)[PER]) {
       float v[PER];

@@ -290,3 +290,22 @@ def test_gradient_against_differences():
             diff = (call(up) - call(down)).item() / real
             # The third derivative over six times the step squared: below 30 here.
             assert abs(grad.view(-1)[i].item() - diff) <= noise + 30 * step ** 2
+
+
+def test_no_columns_and_no_eps():
+    scale = torch.full((3,), CANARY, device="cuda")
+    fg.rms_norm(torch.empty(3, 0, device="cuda"), None, Q=torch.empty(3, 0, dtype=torch.int8, device="cuda"), scale=scale, eps=0.0)
+    assert (scale == 0).all()
+
+
+@pytest.mark.parametrize("K", [40, 3000, 20000])
+def test_gradient_of_huge_and_tiny_rows(K):
+    g = gen(K + 2)
+    size = torch.tensor([1e38, 1e37, 1e-38, 1e-37, 1e30, 1.0], device="cuda")[:, None]
+    h = size * (1 + torch.rand(6, K, device="cuda", generator=g))
+    # Gradients that keep dX among the ordinary numbers, where half a step is relative.
+    dy = torch.randn(6, K, device="cuda", generator=g) * size.clamp(1e-18, 1e18)
+    w = 1 + 0.3 * torch.randn(K, device="cuda", generator=g)
+    dx, dw = torch.empty_like(h), torch.empty(K, device="cuda")
+    fg.rms_norm_grad(dy, h, w, dx, dw, eps=0.0)
+    check_gradient(dy, h, w, None, 0.0, dx, dw)
