@@ -786,16 +786,7 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) 
     // products are where every die sees them once the stores are done, which each
     // wave waits for before the barrier.
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    if (threadIdx.x == 0) last_blocks = 0;
     __syncthreads();
-    const int mine = end - begin;
-    for (int i = threadIdx.x; i < mine; i += kThreads) {
-      const int block = (begin + i) % blocks;
-      if (entries == 0 || atomicAdd(&p.finished[block], 1) == entries - 1) {
-        const int at = atomicAdd(&last_blocks, 1);
-        if (at < kThreads) table.done[at] = block;
-      }
-    }
     const int pairs = p.T * p.top;
     for (int i = threadIdx.x; i < pairs; i += kThreads) {
       const int e = p.ids[i], t = i / p.top;
@@ -807,50 +798,60 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) 
       lds.choice.pair[i] = static_cast<short>(k);
       lds.choice.share[i] = p.share[i];
     }
-    __syncthreads();
-    if (last_blocks == 0) return;
-    // Four columns a thread and four such at a time, so that their loads overlap.
-    const int row_quads = per / 4, quads = last_blocks * row_quads * p.T;  // token by token within a block
-    for (int i0 = threadIdx.x; i0 < quads; i0 += 4 * kThreads) {
-      const float* from[4];
-      int col[4], token[4];
-      rf4 y[4] = {};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = min(i0 + k * kThreads, quads - 1);
-        token[k] = i / row_quads % p.T;
-        col[k] = table.done[i / (row_quads * p.T)] * per + i % row_quads * 4;
-        from[k] = p.z + min(col[k], (wide - 1) / 4 * 4);  // rows of z are whole lines
+    // As many blocks at a time as `done` holds.
+    for (int at0 = begin; at0 < end; at0 += kThreads) {
+      if (threadIdx.x == 0) last_blocks = 0;
+      __syncthreads();
+      if (at0 + static_cast<int>(threadIdx.x) < end) {
+        const int block = (at0 + threadIdx.x) % blocks;
+        if (entries == 0 || atomicAdd(&p.finished[block], 1) == entries - 1)
+          table.done[atomicAdd(&last_blocks, 1)] = block;
       }
-      for (int j0 = 0; j0 < p.top; j0 += 2) {
-        rf4 z[2][4];
-        float share[2][4];
+      __syncthreads();
+      // Four columns a thread and four such at a time, so that their loads overlap.
+      const int row_quads = per / 4, quads = last_blocks * row_quads * p.T;  // token by token within a block
+      for (int i0 = threadIdx.x; i0 < quads; i0 += 4 * kThreads) {
+        const float* from[4];
+        int col[4], token[4];
+        rf4 y[4] = {};
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int k = 0; k < 4; ++k) {
+          const int i = min(i0 + k * kThreads, quads - 1);
+          token[k] = i / row_quads % p.T;
+          col[k] = table.done[i / (row_quads * p.T)] * per + i % row_quads * 4;
+          from[k] = p.z + min(col[k], (wide - 1) / 4 * 4);  // rows of z are whole lines
+        }
+        for (int j0 = 0; j0 < p.top; j0 += 2) {
+          rf4 z[2][4];
+          float share[2][4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int c = token[k] * p.top + min(j0 + j, p.top - 1), pair = lds.choice.pair[c];
-            const bool there = pair >= 0 && j0 + j < p.top;
-            share[j][k] = there ? lds.choice.share[c] : 0.0f;
-            z[j][k] = published(from[k] + (there ? pair : 0) * p.ldz);
-            if (!there) z[j][k] = rf4{};
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int c = token[k] * p.top + min(j0 + j, p.top - 1), pair = lds.choice.pair[c];
+              const bool there = pair >= 0 && j0 + j < p.top;
+              share[j][k] = there ? lds.choice.share[c] : 0.0f;
+              z[j][k] = published(from[k] + (there ? pair : 0) * p.ldz);
+              if (!there) z[j][k] = rf4{};
+            }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] += share[j][k] * z[j][k];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (i0 + k * kThreads >= quads) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (col[k] + i >= wide) break;
+            const long long at = token[k] * p.ldy + col[k] + i;
+            if (XE == kElemF32 || p.out32) put<kElemF32>(p.y, at, y[k][i]);
+            else put<XE>(p.y, at, y[k][i]);
           }
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] += share[j][k] * z[j][k];
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (i0 + k * kThreads >= quads) break;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (col[k] + i >= wide) break;
-          const long long at = token[k] * p.ldy + col[k] + i;
-          if (XE == kElemF32 || p.out32) put<kElemF32>(p.y, at, y[k][i]);
-          else put<XE>(p.y, at, y[k][i]);
         }
       }
+      __syncthreads();  // `done` is read
     }
   }
 #endif
@@ -887,6 +888,7 @@ __global__ __launch_bounds__(kThreads, 2) void expert_out_kernel(const LayerArgs
     few.entry(v, e, set);
     e = __builtin_amdgcn_readfirstlane(e);
     const int n = __builtin_amdgcn_readfirstlane(few.list_pairs(e, 16 * set, list, lane));
+    if (n == 0) continue;  // the rest of e's pairs were a token's second ones: `list` holds nothing
     const int pair = list[lane % 16 < n ? lane % 16 : 0], token = pair / p.top;
     float share = 0.0f;  // of all the token's choices of e
     for (int j = token * p.top; j < (token + 1) * p.top; ++j) share += p.ids[j] == e ? p.share[j] : 0.0f;

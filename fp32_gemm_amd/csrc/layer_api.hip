@@ -250,7 +250,7 @@ int expert_layer(int32_t type, int32_t weights, int32_t out_type, int32_t gated,
   a.D = static_cast<int>(D);
   a.F = static_cast<int>(F);
   a.experts = experts;
-  a.top = top;
+  a.top = work ? top : 0;  // without a hidden width nothing is read, and Y is zeros
   a.gated = gated;
   a.out32 = out_type == GEMM_F32;
   return launched(expert_layer_launch(type, weights, a, static_cast<hipStream_t>(stream)));

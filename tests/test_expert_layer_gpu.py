@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import fp32_gemm_amd as fg
+from fp32_gemm_amd.binding import _lib
 from test_mx4_gpu import unpack
 
 pytestmark = pytest.mark.gpu
@@ -66,7 +67,7 @@ def reference(x, ids, share, w_in, w_out, gated, held, scaled, terms=None):
     return y, off
 
 
-def run(case, seed=0, ids=None, out=None, strides=None):
+def run(case, seed=0, ids=None, out=None, strides=None, terms=None):
     dtype, kind, gated, E, T, top, D, F = case
     g = gen(seed)
     x = torch.randn(T, D, device="cuda", generator=g).to(dtype)
@@ -79,7 +80,7 @@ def run(case, seed=0, ids=None, out=None, strides=None):
     if strides:
         x, w_in, w_out, y = strides(x, w_in, w_out, y)
     assert fg.expert_layer(x, ids, share, w_in, w_out, y, s_in, s_out, gated=gated) is y
-    want, off = reference(x, ids, share, v_in, v_out, gated, dtype, kind == "int8")
+    want, off = reference(x, ids, share, v_in, v_out, gated, dtype, kind == "int8", terms)
     bound = off + HALF_STEP[y.dtype] * (want.abs() + off) + TINY[y.dtype]
     assert ((y.double() - want).abs() <= bound).all()
     return y
@@ -235,3 +236,42 @@ def test_every_place_counts_once(dtype, kind, E, T, top, D, F):
     fg.expert_layer(x, ids, share, w_in, w_out, y, s_in, s_out)
     want, off = reference(x, ids, share, v_in, v_out, True, dtype, kind == "int8", terms=(few, few))
     assert ((y.double() - want).abs() <= off * (1 + 2.0 ** -20) + 2.0 ** -24 * want.abs() + TINY[F32]).all()
+
+
+@pytest.mark.parametrize("kind", ["same", "int8", "mx4"])
+@pytest.mark.parametrize("T,top", [(1, 40), (1, 128), (4, 20), (16, 8), (3, 170)])
+def test_the_same_expert_many_times(kind, T, top):
+    # More pairs than tokens: an expert's second sets of 16 pairs hold no token.  The sum
+    # over the choices rounds `top` times more.
+    g = gen(top)
+    for used in (1, 2):
+        ids = torch.randint(0, used, (T, top), device="cuda", generator=g, dtype=torch.int32)
+        run((BF16, kind, True, 4, T, top, 96, 64), ids=ids, out=F32, terms=(96, 64 + top))
+
+
+def test_more_columns_than_a_workgroup_lists():
+    # 256 experts of 2048 blocks of columns each: a late workgroup is the last at
+    # hundreds of them.
+    E, D = 256, 1 << 18
+    g = gen(12)
+    x = torch.randn(1, D, device="cuda", generator=g).bfloat16()
+    w_in = (torch.randn(E, 1, D, device="cuda", generator=g) * 2.0 ** -9).bfloat16()
+    w_out = torch.randn(E, D, 1, device="cuda", generator=g).bfloat16()
+    ids = torch.randperm(E, device="cuda", generator=g).to(torch.int32)[None]
+    share = torch.rand(1, E, device="cuda", generator=g)
+    want, off = reference(x, ids, share, w_in.double(), w_out.double(), False, BF16, False, (D, 1 + E))
+    y = torch.full((1, D), 777.0, device="cuda")
+    fg.expert_layer(x, ids, share, w_in, w_out, y, gated=False)
+    assert ((y.double() - want).abs() <= off + HALF_STEP[F32] * (want.abs() + off) + TINY[F32]).all()
+
+
+@pytest.mark.parametrize("T,top", [(3, 2), (20, 2), (64, 8)])
+@pytest.mark.parametrize("weights", [1, 3, 5])
+def test_no_hidden_width_and_no_operands(T, top, weights):
+    y = torch.full((T, 40), 777.0, device="cuda")
+    room = torch.empty(_lib.expert_layer_workspace(1, T, 40, 0, top), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert _lib.expert_layer(1, weights, 0, 1, T, 40, 0, 4, top, None, 40, None, None, None, 40, 0, None, None, 1, 0, None,
+                             y.data_ptr(), 40, room.data_ptr(), room.numel(), None) == 0
+    torch.cuda.synchronize()
+    assert (y == 0).all()
