@@ -15,10 +15,10 @@
 // an expert's rows.
 //
 // Measured, for the layer of 4096 by 2048 with a gate: one token, 2 of 16 experts in
-// bf16 28 us (3.6 TB/s over both kernels), 64 tokens, 16 experts in 8 bits 108 us
-// (3.6 TB/s), in bf16 168 us (4.8 TB/s).  The first kernel streams 5 TB/s once it is
-// under way; each kernel begins with some 8 us of latency (ids, first weights and
-// values) in which it reads little.
+// bf16 27 us (3.7 TB/s over both kernels), 64 tokens, 16 experts in 8 bits 101 us
+// (3.8 TB/s), in bf16 165 us (4.9 TB/s).  The kernels stream 5 TB/s once they are
+// under way; what is left is each kernel's start (launch, ids, first loads: 5 us in
+// which little arrives) and the last sums (3 us, 6 for 64 tokens).
 //
 // The second kernel leaves an expert's products, not yet shared out, for each pair
 // of token and choice; the last workgroup to finish a block of columns adds them up
@@ -216,6 +216,9 @@ struct Format {
 };
 
 __device__ __forceinline__ rb8 weights_of_8_bits(int lo, int hi) {
+  // Whole words until here: seen as bytes, they would be taken apart, and waited for,
+  // where they are loaded.
+  asm("" : "+v"(lo), "+v"(hi));
   rb8 r;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -276,8 +279,8 @@ __device__ __forceinline__ void layer_mma(rf4& acc, const ri4& w, const ri4* x, 
   }
 }
 
-// A wave's part of an expert's rows: NB blocks of 16 rows at a time, U steps of
-// them on their way and U more in hand.
+// A wave's part of an expert's rows: NB blocks of 16 rows at a time, a turn of U steps
+// of them in hand and one or two more on their way.
 //   Q > 0   the tokens' values stay in registers for all rows: Q turns of U steps
 //           are all that the wave has of the reduction.
 //   Q == 0  they are loaded again with each turn.
@@ -496,11 +499,21 @@ struct Rows {
       }
     }
   }
-  // Blocks lo .. hi - 1; calls end(block, acc) for each, by all waves alike.
+  // Begins to load the second turn of blocks lo .. hi - 1 and waits for the values, which
+  // were sent before it: loads arrive in their order.
+  __device__ __forceinline__ void load_second(Held& b, int lo, int hi) const {
+    if (lo + 1 / XT < hi) {
+      load(b, lo + 1 / XT, 1 % XT);
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(U * NB + (Fm::BLOCKS ? NB : 0)) : "memory");  // or more
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+  }
+  // Blocks lo .. hi - 1; calls end(block, acc) for each, by all waves alike.  `a` holds
+  // the first turn, and where values are kept `b` the second one.
   template <class F>
-  __device__ __forceinline__ void run(int lo, int hi, Held& a, F end) {
+  __device__ __forceinline__ void run(int lo, int hi, Held& a, Held& b, F end) {
     rf4 acc[NB] = {};
-    Held b;
     Rest rest;
     auto begin = [&](int block) {
       if constexpr (Fm::SAME)
@@ -521,16 +534,17 @@ struct Rows {
     };
     if constexpr (KEPT) {
       // The turns of a block, or of two, are written out, so that each knows its
-      // registers.
+      // registers.  Two are on their way while one is multiplied or its sums are
+      // shared (one: 8 tokens, 2 choices of 32, 4 bits, 4096 by 2048: 52 us for 46).
       constexpr int BLOCKS = Q % 2 ? 2 : 1;
       for (int block = lo; block < hi; block += BLOCKS) {
 #pragma unroll
         for (int i = 0; i < BLOCKS * Q; ++i) {
-          const int now = block + i / Q, next = block + (i + 1) / Q;
+          const int now = block + i / Q, next = block + (i + 2) / Q;
           if (now < hi) {
             if (i % Q == 0) begin(now);
-            if (next < hi) load(i % 2 ? a : b, next, (i + 1) % Q);
             multiply(acc, i % 2 ? b : a, i % Q);
+            if (next < hi) load(i % 2 ? b : a, next, (i + 2) % Q);
             if (i % Q == Q - 1) done(now);
           }
         }
@@ -610,7 +624,7 @@ __device__ __forceinline__ void meet_in_lds() {
 template <int XE, int WE>
 struct Kept {
   static constexpr int XV = Format<XE, WE>::XV, PARTS = Format<XE, WE>::PARTS, PIECES = PARTS == 1 ? 16 : 8;
-  static constexpr int U = PIECES / XV < 4 ? PIECES / XV : PARTS == 1 && WE != kElemI8 ? 4 : 2, MOST = PIECES / (U * XV);
+  static constexpr int U = PIECES / XV < 4 ? PIECES / XV : PARTS == 1 ? 4 : 2, MOST = PIECES / (U * XV);
 };
 
 // One of the two products.
@@ -661,8 +675,8 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) 
   // This workgroup's units, a block of an entry each; where nothing is used, y alone
   // is left to be written, block by block.  Each entry that a workgroup begins costs
   // it a few microseconds of latency, so the entries get whole workgroups where that
-  // leaves few over (32 experts, 16 tokens, 4 choices, 8 bits, 2048 by 1024: 94 us
-  // with units in equal runs whatever the entry).
+  // leaves few over (32 experts, 16 tokens, 4 choices, 8 bits, 2048 by 1024: 54 us,
+  // and 63 with units in equal runs whatever the entry).
   const int owners = max(entries, IN ? 0 : 1), group = blockIdx.x;
   const int each = owners > 0 ? kGroups / owners : 0;
   int begin = 0, end = 0;  // fewer than 2^24 in all: 512 entries of 2^15 blocks
@@ -728,7 +742,7 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) 
         r.rows[b] = (IN ? p.w_in + e * p.stride_in : p.w_out + e * p.stride_out) + row * r.ld;
         r.scales[b] = static_cast<const char*>(scale_all) + (static_cast<long long>(e) * rows_of + row) * scale_blocks;
       }
-      typename R::Held held;
+      typename R::Held held, second;
       if constexpr (R::KEPT) r.load(held, lo, 0);  // weights first, they take longest
       const int n = find();
       const int pair = list[lane % 16 < n ? lane % 16 : 0];
@@ -738,13 +752,13 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) 
       if constexpr (R::KEPT) {
         const rlds_t room = (rlds_t)&lds.values[wave][0];
         r.send_values(room, n, list, IN ? p.top : 1, IN ? p.ldx : p.ldh);
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        r.load_second(second, lo, hi);
         r.keep_values(room, n);
         meet_in_lds();  // sums may take their place
       } else {
         r.load(held, lo, 0);
       }
-      r.run(lo, hi, held, [&](int block, rf4 (&acc)[2]) {
+      r.run(lo, hi, held, second, [&](int block, rf4 (&acc)[2]) {
         float (&sums)[kWaves][2][16][kRows + 1] = lds.sums[block & 1];
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -785,8 +799,6 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) 
     // The last workgroup at a block of columns adds up each token's choices.  The
     // products are where every die sees them once the stores are done, which each
     // wave waits for before the barrier.
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
     const int pairs = p.T * p.top;
     for (int i = threadIdx.x; i < pairs; i += kThreads) {
       const int e = p.ids[i], t = i / p.top;
@@ -798,6 +810,8 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) 
       lds.choice.pair[i] = static_cast<short>(k);
       lds.choice.share[i] = p.share[i];
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
     // As many blocks at a time as `done` holds.
     for (int at0 = begin; at0 < end; at0 += kThreads) {
       if (threadIdx.x == 0) last_blocks = 0;
@@ -808,26 +822,27 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) 
           table.done[atomicAdd(&last_blocks, 1)] = block;
       }
       __syncthreads();
-      // Four columns a thread and four such at a time, so that their loads overlap.
+      // Four columns a thread and two such at a time (four: up to a microsecond more).
+      constexpr int QUADS = 2;
       const int row_quads = per / 4, quads = last_blocks * row_quads * p.T;  // token by token within a block
-      for (int i0 = threadIdx.x; i0 < quads; i0 += 4 * kThreads) {
-        const float* from[4];
-        int col[4], token[4];
-        rf4 y[4] = {};
+      for (int i0 = threadIdx.x; i0 < quads; i0 += QUADS * kThreads) {
+        const float* from[QUADS];
+        int col[QUADS], token[QUADS];
+        rf4 y[QUADS] = {};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < QUADS; ++k) {
           const int i = min(i0 + k * kThreads, quads - 1);
           token[k] = i / row_quads % p.T;
           col[k] = table.done[i / (row_quads * p.T)] * per + i % row_quads * 4;
           from[k] = p.z + min(col[k], (wide - 1) / 4 * 4);  // rows of z are whole lines
         }
         for (int j0 = 0; j0 < p.top; j0 += 2) {
-          rf4 z[2][4];
-          float share[2][4];
+          rf4 z[2][QUADS];
+          float share[2][QUADS];
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < QUADS; ++k) {
               const int c = token[k] * p.top + min(j0 + j, p.top - 1), pair = lds.choice.pair[c];
               const bool there = pair >= 0 && j0 + j < p.top;
               share[j][k] = there ? lds.choice.share[c] : 0.0f;
@@ -837,10 +852,10 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) 
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] += share[j][k] * z[j][k];
+            for (int k = 0; k < QUADS; ++k) y[k] += share[j][k] * z[j][k];
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < QUADS; ++k) {
           if (i0 + k * kThreads >= quads) break;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -860,9 +875,10 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) 
 // The second product where few experts are used: a workgroup takes 16 columns of y
 // for all tokens, its waves divide the used experts' rows, end to end, and what each
 // finds for a token it adds up in LDS.  No workgroup waits for another's products
-// (one token, 2 of 16 experts, bf16, 4096 by 2048: the layer takes 28 us so, 33 with
-// the kernel above); with more experts than waves each wave has too many short
-// pieces (8 tokens, 2 choices of 32: 24 us and 19).
+// (one token, 2 of 16 experts, 4096 by 2048: the layer takes 27 us so in bf16 and 16
+// in 4 bits, 31 and 20 with the kernel above); with more experts than waves each wave
+// has too many short pieces (8 bits, 2048 by 1024, 16 tokens, 4 choices of 32: 70 us
+// and 54).
 constexpr int kDirectTokens = 16, kDirectExperts = kWaves;
 template <int XE, int WE>
 __global__ __launch_bounds__(kThreads, 2) void expert_out_kernel(const LayerArgs p) {
@@ -915,9 +931,9 @@ __global__ __launch_bounds__(kThreads, 2) void expert_out_kernel(const LayerArgs
       scale[i] = WE == kElemI8 ? static_cast<const float*>(p.scale_out)[static_cast<long long>(e) * p.D +
                                                                         min(block * 16 + lane / 16 * 4 + i, p.D - 1)]
                                : 1.0f;
-    typename R::Held held;
+    typename R::Held held, second;
     r.load(held, block, 0);
-    r.run(block, block + 1, held, [&](int, rf4 (&acc)[1]) {
+    r.run(block, block + 1, held, second, [&](int, rf4 (&acc)[1]) {
       if (lane % 16 < n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) sums[wave][token][lane / 16 * 4 + i] += acc[0][i] * scale[i] * share;
