@@ -906,8 +906,6 @@ __global__ __launch_bounds__(kThreads, 2) void expert_out_kernel(const LayerArgs
     const int n = __builtin_amdgcn_readfirstlane(few.list_pairs(e, 16 * set, list, lane));
     if (n == 0) continue;  // the rest of e's pairs were a token's second ones: `list` holds nothing
     const int pair = list[lane % 16 < n ? lane % 16 : 0], token = pair / p.top;
-    float share = 0.0f;  // of all the token's choices of e
-    for (int j = token * p.top; j < (token + 1) * p.top; ++j) share += p.ids[j] == e ? p.share[j] : 0.0f;
     R r;
     r.lane = lane;
     r.ld = p.ldw_out;
@@ -933,6 +931,8 @@ __global__ __launch_bounds__(kThreads, 2) void expert_out_kernel(const LayerArgs
                                : 1.0f;
     typename R::Held held, second;
     r.load(held, block, 0);
+    float share = 0.0f;  // of all the token's choices of e
+    for (int j = token * p.top; j < (token + 1) * p.top; ++j) share += p.ids[j] == e ? p.share[j] : 0.0f;
     r.run(block, block + 1, held, second, [&](int, rf4 (&acc)[1]) {
       if (lane % 16 < n)
 #pragma unroll
