@@ -275,3 +275,32 @@ def test_no_hidden_width_and_no_operands(T, top, weights):
                              y.data_ptr(), 40, room.data_ptr(), room.numel(), None) == 0
     torch.cuda.synchronize()
     assert (y == 0).all()
+
+
+@pytest.mark.parametrize("dtype,kind", [(F32, "same"), (BF16, "mx4"), (BF16, "int8")])
+@pytest.mark.parametrize("D,F", [(1 << 19, 3), (5, 1 << 19)])
+def test_the_widest_layers(dtype, kind, D, F):
+    # 64 tokens of 8 choices: a token's values and products lie furthest apart.  Values
+    # and weights that are zero but at a few places keep the sums short.
+    g, T, top, E = gen(D % 1000), 64, 8, 2
+    w_in, s_in, v_in = make_weights(g, kind, E, 2 * F, D, dtype)
+    w_out, s_out, v_out = make_weights(g, kind, E, D, F, dtype)
+    x = torch.zeros(T, D, device="cuda", dtype=dtype)
+    n = min(D, 4)
+    places = torch.cat([torch.tensor([0, D - 1], device="cuda"), torch.randint(0, D, (n - 2,), device="cuda", generator=g)])
+    x[:, places] = torch.randn(T, n, device="cuda", generator=g).to(dtype)
+    keep = torch.zeros(F, dtype=torch.bool, device="cuda")
+    keep[torch.tensor([0, F // 2, F - 1], device="cuda")] = True
+    v_out = torch.where(keep, v_out, 0.0)
+    if kind == "mx4":
+        pairs = torch.nn.functional.pad(keep, (0, F % 2)).view(-1, 2)
+        w_out &= (pairs[:, 0] * 15 + pairs[:, 1] * 240).to(torch.uint8)
+    else:
+        w_out[..., ~keep] = 0
+    ids = torch.full((T, top), -1, dtype=torch.int32, device="cuda")
+    ids[::7, -1], ids[-1, 0], ids[-1, 3] = 1, 0, 1
+    share = torch.rand(T, top, device="cuda", generator=g)
+    y = torch.full((T, D), 777.0, device="cuda")
+    fg.expert_layer(x, ids, share, w_in, w_out, y, s_in, s_out)
+    want, off = reference(x, ids, share, v_in, v_out, True, dtype, kind == "int8", (n, 3 + top))
+    assert ((y.double() - want).abs() <= off * (1 + 2.0 ** -20) + 2.0 ** -24 * want.abs() + TINY[F32]).all()

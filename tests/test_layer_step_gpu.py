@@ -316,3 +316,17 @@ def test_the_norm_as_a_torch_function():
 def test_serving_in_4_bits():
     _, _, errors = expert_layer.main(width=256, hidden=512, tokens=256, steps=2, bits=4)
     assert all(e == e for e in errors)
+
+
+def test_the_default_stream_by_its_handle():
+    s = Step(*SIZES[0], seed=12)
+    s.run()
+    want = s.outputs()
+    s.y.fill_(float("nan"))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()) as _:
+        now = torch.cuda.current_stream()
+        fg.expert_layer(s.b, s.ids, s.share, s.w_in, s.w_out, s.y, s.s_in, s.s_out, stream=0)
+        assert torch.cuda.current_stream() == now
+    torch.cuda.synchronize()
+    assert torch.equal(s.y, want[-1])

@@ -305,3 +305,26 @@ def test_quantized_products_stand_for_the_rows():
         return (b / 4).repeat_interleave(32, 1)[:, :v.shape[1]]
     assert ((unpack(q, s)[:, :515] - x.double()).abs() <= worst(x)).all()
     assert ((unpack(p, t)[:, :515] - w.double()).abs() <= worst(w)).all()
+
+
+@pytest.mark.parametrize("M,N", [(3, 5), (40, 70), (700, 600)])
+def test_the_longest_reduction(M, N):
+    # Rows of 2^22 - 2 values that are zero but for one byte in each of a few blocks, the
+    # first and the last among them: the sums are exact.
+    g = gen(M)
+    K2 = (1 << 21) - 1
+    at = torch.cat([torch.tensor([0, K2 - 1], device="cuda"), 16 * torch.randperm(K2 // 16 - 2, device="cuda", generator=g)[:6] + 19])
+    block, inside = at // 16, at % 16
+    wide, short = [], []
+    for rows in (M, N):
+        codes = torch.randint(0, 256, (rows, len(at)), dtype=torch.uint8, device="cuda", generator=g)
+        s = torch.randint(126, 129, (rows, len(at)), dtype=torch.uint8, device="cuda", generator=g)
+        q, scale = torch.zeros(rows, K2, dtype=torch.uint8, device="cuda"), torch.full((rows, (K2 + 15) // 16), 127, dtype=torch.uint8, device="cuda")
+        q[:, at], scale[:, block] = codes, s
+        p = torch.zeros(rows, len(at), 16, dtype=torch.uint8, device="cuda")
+        p[:, torch.arange(len(at), device="cuda"), inside] = codes
+        wide += [q, scale]
+        short += [p.view(rows, -1), s]
+    y = torch.full((M, N), 777.0, device="cuda")
+    fg.gemm_mx4(*wide, y)
+    assert torch.equal(y.double(), product(*short, None)[0])
