@@ -165,23 +165,24 @@ constexpr double kTie = 0x1p-40;
 
 constexpr int kNormBlocks = 1 << 23;  // workgroups in x; more rows go on in y
 
-// One row by THREADS threads of 256, KEEP pieces a thread in registers as they
-// came; longer rows are read again.  H may be x or r itself: a thread has read
+// One row by THREADS threads of a workgroup of 256 or as many, KEEP pieces a thread in
+// registers as they came; longer rows are read again.  H may be x or r itself: a thread has read
 // what it overwrites, and where rows are read twice, H is written the second time.
 // Memory-bound without codes: bf16 8192 x 8192 with a residual 102 us, 5.3 TB/s, as a
 // copy runs.  With codes as well bound by the two reductions' latencies: 103 us for
 // 7 bytes a value, 4.6 TB/s (weights read again for the codes: 114; the largest |v|
 // in 64 bits throughout, and a division for every value near a tie: 116).
 template <int ELEM, bool W32, int THREADS, int KEEP, bool CODES>
-__global__ __launch_bounds__(256) void rms_norm_kernel(const NormArgs p) {
+__global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_kernel(const NormArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
+  constexpr int ROWS = THREADS < 256 ? 256 / THREADS : 1;  // of a workgroup
   using P = Piece<ELEM>;
   using W = Weights<ELEM, W32>;
   constexpr int ES = elem_size(ELEM), PER = P::PER;
-  __shared__ double room[2][4][2];
+  __shared__ double room[2][THREADS / 64][2];
   const int in = threadIdx.x % THREADS;
   const long long block = static_cast<long long>(blockIdx.y) * kNormBlocks + blockIdx.x;
-  const long long row = block * (256 / THREADS) + threadIdx.x / THREADS;
+  const long long row = block * ROWS + threadIdx.x / THREADS;
   const bool live = row < p.M;  // uniform in a wave
   const char* const x = p.x + (live ? row : 0) * p.ldx * ES;
   const char* const r = p.r == nullptr ? nullptr : p.r + (live ? row : 0) * p.ldr * ES;
@@ -512,15 +513,23 @@ template <int ELEM, bool W32>
 hipError_t launch_norm(const NormArgs& args, hipStream_t s) {
   // A wave takes rows of up to two pieces a lane, and where there are rows enough for
   // all waves of up to eight, or four with codes (16384 x 4096, residual and codes:
-  // 111 us with eight, 96 by four waves); longer ones go to four waves.
+  // 111 us with eight, 96 by four waves); longer ones go to four waves, or, where
+  // few rows leave the card idle and a row's instructions are what takes time, to eight
+  // or sixteen (bf16 with codes: 1 x 4096 3.8 us, and 4.2 by four waves, 256 x 16384 12.6
+  // and 17.3, but 512 x 8192 14.1 and 12.4; without 1 x 16384 4.4 and 7.8, 512 x 8192 8.7
+  // and 9.9, but 1024 x 8192 15.0 and 13.9).
   const int pieces = args.K / Piece<ELEM>::PER;
   const bool codes = args.scale != nullptr;
   const bool wave = pieces <= 128 || (pieces <= (codes ? 256 : 512) && args.M >= 4096);
-  const int each = wave ? (pieces + 63) / 64 : (pieces + 255) / 256;
+  const bool wide = !wave && args.M <= (codes ? 256 : 512) && pieces > 256 && pieces <= 2048;
+  const int threads = wave ? 64 : !wide ? 256 : pieces <= 512 ? 512 : 1024, each = (pieces + threads - 1) / threads;
   const void* const kernel = wave ? (each <= 1   ? norm_kernel<ELEM, W32, 64, 1>(codes)
                                      : each <= 2 ? norm_kernel<ELEM, W32, 64, 2>(codes)
                                      : each <= 4 ? norm_kernel<ELEM, W32, 64, 4>(codes)
                                                  : norm_kernel<ELEM, W32, 64, 8>(codes))
+                             : wide ? (pieces <= 512    ? norm_kernel<ELEM, W32, 512, 1>(codes)
+                                       : pieces <= 1024 ? norm_kernel<ELEM, W32, 1024, 1>(codes)
+                                                        : norm_kernel<ELEM, W32, 1024, 2>(codes))
                                   : (each <= 1   ? norm_kernel<ELEM, W32, 256, 1>(codes)
                                      : each <= 2 ? norm_kernel<ELEM, W32, 256, 2>(codes)
                                      : each <= 4 ? norm_kernel<ELEM, W32, 256, 4>(codes)
@@ -529,7 +538,7 @@ hipError_t launch_norm(const NormArgs& args, hipStream_t s) {
   const dim3 grid(blocks < kNormBlocks ? blocks : kNormBlocks, (blocks + kNormBlocks - 1) / kNormBlocks);
   NormArgs a = args;
   void* values[] = {&a};
-  return hipLaunchKernel(kernel, grid, dim3(256), values, 0, s);
+  return hipLaunchKernel(kernel, grid, dim3(wide ? threads : 256), values, 0, s);
 }
 
 template <int ELEM, bool W32>

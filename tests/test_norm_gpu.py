@@ -309,3 +309,10 @@ def test_gradient_of_huge_and_tiny_rows(K):
     dx, dw = torch.empty_like(h), torch.empty(K, device="cuda")
     fg.rms_norm_grad(dy, h, w, dx, dw, eps=0.0)
     check_gradient(dy, h, w, None, 0.0, dx, dw)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("M", [256, 512, 513])
+@pytest.mark.parametrize("K", [2100, 3001, 6005, 12000, 18003])
+def test_long_rows_few_and_many(dtype, M, K):
+    test_norm(dtype, M, K)
