@@ -71,7 +71,8 @@ int64_t rms_norm_grad_workspace(int64_t M, int64_t K); /* -1 for sizes out of ra
  * silu(u[0:F]) * u[F:2F]; with gated == 0 it is F x D and h = silu.  W_out[e] is D x F.
  * X is T x D of `type`, Y T x D of out_type, `type` or GEMM_F32.  ids and share are
  * T x top, tight, on the device.  An id outside 0 .. experts - 1 names no expert; a token
- * without any gets zeros.  A token may name an expert more than once.
+ * without any gets zeros.  A token may name an expert more than once.  Where F == 0 Y is
+ * zeros and nothing is read.
  * weights: the weights' format.  `type` itself; 3: 8-bit integers with a float scale for each
  * row (scale_in experts x 2 F or F, scale_out experts x D), as quantize_rows writes
  * them; 5: microscaled 4-bit floats (leading dimensions and strides in bytes, scales
