@@ -15,10 +15,16 @@
 // an expert's rows.
 //
 // Measured, for the layer of 4096 by 2048 with a gate: one token, 2 of 16 experts in
-// bf16 27 us (3.7 TB/s over both kernels), 64 tokens, 16 experts in 8 bits 101 us
-// (3.8 TB/s), in bf16 165 us (4.9 TB/s).  The kernels stream 5 TB/s once they are
+// bf16 28 us (3.6 TB/s over both kernels), 64 tokens, 16 experts in 8 bits 105 us
+// (3.6 TB/s), in bf16 165 us (4.9 TB/s).  The kernels stream 5 TB/s once they are
 // under way; what is left is each kernel's start (launch, ids, first loads: 5 us in
 // which little arrives) and the last sums (3 us, 6 for 64 tokens).
+//
+// Between the two, h is held in 32 bits: as a float where the tokens are floats, else as
+// a sum of two bf16, to 2^-17 of itself and with the range of a float.  The matrix
+// instruction takes such parts as they lie (rounded to the tokens' type instead, h was
+// what results were off by, 2.3e-3 for 1.7e-3, and infinite past 65504 in f16; that took
+// 1 us less for one token in bf16, 3 for 64 in 8 bits).
 //
 // The second kernel leaves an expert's products, not yet shared out, for each pair
 // of token and choice; the last workgroup to finish a block of columns adds them up
@@ -26,6 +32,8 @@
 #include "expert_layer.hpp"
 
 #include "ragged_kernels.hpp"
+
+#include <algorithm>
 
 namespace fp32gemm {
 namespace {
@@ -201,17 +209,25 @@ struct Routing {
 };
 
 // ---------------------------------------------------------------------------
+// Values that are sums of two bf16: eight first parts, then the eight second ones; rows
+// are filled up with zeros to a multiple of eight.
+constexpr int kElemPair = 6;
+// h, of tokens of type XE.
+template <int XE>
+constexpr int kHidden = XE == kElemF32 ? kElemF32 : kElemPair;
+
 // How weights of format WE and values of type XE are multiplied.
 template <int XE, int WE>
 struct Format {
   static constexpr bool SAME = XE == WE, BLOCKS = WE == kElemM4;
-  static constexpr int XS = elem_size(XE);
+  static constexpr bool PAIR = XE == kElemPair, HALVES = PAIR && (WE == kElemBF16 || WE == kElemF16);
+  static constexpr int XS = PAIR ? 4 : elem_size(XE);
   static constexpr int PER = WE == kElemM4 ? 32 : 16 / elem_size(WE);  // weights of 16 bytes
   static constexpr int STEP = 4 * PER;                                  // of a step
   static constexpr int XV = PER * XS / 16;                              // 16-byte pieces of values for them
   // Narrow weights become bf16, exactly; values become a sum of one, two or
   // three bf16, exactly too, and are multiplied one after another.
-  static constexpr int PARTS = SAME ? 1 : XE == kElemBF16 ? 1 : XE == kElemF16 ? 2 : 3;
+  static constexpr int PARTS = SAME ? 1 : XE == kElemBF16 ? 1 : XE == kElemF16 || PAIR ? 2 : 3;
   static constexpr int MMAS = SAME ? 1 : PER / 8;
 };
 
@@ -234,11 +250,27 @@ __device__ __forceinline__ rb8 weights_of_4_bits(unsigned codes, float scale) {
   return rb8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// Eight weights of f16 as a sum of two bf16, neither of them zero unless the weight is, so
+// that an infinite value times the weight is infinite.
+__device__ __forceinline__ void weights_of_f16(const ri4& w, rb8 (&part)[2]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = static_cast<float>(__builtin_bit_cast(rh8, w)[i]);
+    float top = __builtin_bit_cast(float, __builtin_bit_cast(unsigned, v) & 0xFFFF0000u), rest = v - top;
+    if (!(__builtin_fabsf(rest) > 0.0f)) top = rest = 0.5f * v;  // eight bits or fewer, or no number
+    part[0][i] = __builtin_bit_cast(__bf16, static_cast<unsigned short>(__builtin_bit_cast(unsigned, top) >> 16));
+    part[1][i] = __builtin_bit_cast(__bf16, static_cast<unsigned short>(__builtin_bit_cast(unsigned, rest) >> 16));
+  }
+}
+
 // Eight values as a sum of bf16.
 template <int XE, int PARTS>
 __device__ __forceinline__ void split_values(const ri4* raw, int m, rb8 (&part)[PARTS]) {
   if constexpr (XE == kElemBF16) {
     part[0] = __builtin_bit_cast(rb8, raw[m]);
+  } else if constexpr (XE == kElemPair) {
+    part[0] = __builtin_bit_cast(rb8, raw[2 * m]);
+    part[1] = __builtin_bit_cast(rb8, raw[2 * m + 1]);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -266,12 +298,25 @@ __device__ __forceinline__ void layer_mma_8(rf4& acc, int lo, int hi, const ri4*
 #pragma unroll
   for (int k = 0; k < Fm::PARTS; ++k) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, part[k], acc, 0, 0, 0);
 }
+// Eight weights of 16 bits times eight sums of two bf16.
+template <int WE>
+__device__ __forceinline__ void layer_mma_pairs(rf4& acc, const ri4& w, const ri4* x) {
+  rb8 wb[2] = {__builtin_bit_cast(rb8, w), {}};
+  if constexpr (WE == kElemF16) weights_of_f16(w, wb);
+#pragma unroll
+  for (int j = 0; j < (WE == kElemF16 ? 2 : 1); ++j)
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], __builtin_bit_cast(rb8, x[k]), acc, 0, 0, 0);
+}
 // One step of one block of rows and one set of tokens.
 template <int XE, int WE>
 __device__ __forceinline__ void layer_mma(rf4& acc, const ri4& w, const ri4* x, float scale) {
   using Fm = Format<XE, WE>;
   if constexpr (Fm::SAME) {
     ragged_mma<XE, 16>(acc, w, x[0]);
+  } else if constexpr (Fm::HALVES) {
+    layer_mma_pairs<WE>(acc, w, x);
   } else {
 #pragma unroll
     for (int m = 0; m < Fm::MMAS; ++m)
@@ -317,12 +362,15 @@ struct Rows {
   // instruction: loaded as the products take them, each would touch 64 lines.  Piece c
   // of token t lies at place c ^ t of its row, so that the tokens' reads spread over
   // the banks.
-  static constexpr int KEEP_ROW = XT * U * Fm::STEP * Fm::XS;  // bytes of a token
-  static_assert(!KEPT || (KEEP_ROW & (KEEP_ROW - 1)) == 0, "a power of two");
-  __device__ __forceinline__ void send_values(rlds_t room, int n, const short* list, int top, long long ldx) const {
+  // More than 16 pieces a lane come in two passes.
+  static constexpr int PASSES = XT * U * Fm::XV > 16 ? 2 : 1, PASS = XT * U / PASSES;  // steps of one
+  static constexpr int KEEP_ROW = PASS * Fm::STEP * Fm::XS;  // bytes of a token
+  static_assert(!KEPT || ((KEEP_ROW & (KEEP_ROW - 1)) == 0 && PASS * PASSES == XT * U), "a power of two");
+  __device__ __forceinline__ void send_values(rlds_t room, int pass, int n, const short* list, int top,
+                                              long long ldx) const {
     constexpr int PIECES = KEEP_ROW / 16, EACH = PIECES < 64 ? 64 / PIECES : 1;  // tokens an instruction
     const auto v = ragged_rsrc(values, kRaggedMasked);
-    const int end = end_step * Fm::STEP * Fm::XS, start = first_step * Fm::STEP * Fm::XS;
+    const int end = end_step * Fm::STEP * Fm::XS, start = (first_step + pass * PASS) * Fm::STEP * Fm::XS;
     for (int t0 = 0; t0 < n; t0 += EACH)
 #pragma unroll
       for (int part = 0; part < (PIECES + 63) / 64; ++part) {
@@ -334,20 +382,19 @@ struct Rows {
             t < n && at < end ? row + at : kRaggedMasked, 0, 0, 0);
       }
   }
+  template <int P>
   __device__ __forceinline__ void keep_values(rlds_t room, int n) {
     constexpr int PIECES = KEEP_ROW / 16;
     const int t = lane % 16;
 #pragma unroll
-    for (int q = 0; q < XT; ++q)
+    for (int s = 0; s < PASS; ++s)
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < Fm::XV; ++i) {
-          const int piece = ((q * U + u) * 4 + lane / 16) * Fm::XV + i;
-          const ri4 x = *(__attribute__((address_space(3))) ri4*)(room + t * KEEP_ROW +
-                                                                 (piece ^ (t & (PIECES - 1) & 15)) * 16);
-          kept[q][u][i] = t < n ? x : ri4{};
-        }
+      for (int i = 0; i < Fm::XV; ++i) {
+        const int piece = (s * 4 + lane / 16) * Fm::XV + i;
+        const ri4 x = *(__attribute__((address_space(3))) ri4*)(room + t * KEEP_ROW +
+                                                               (piece ^ (t & (PIECES - 1) & 15)) * 16);
+        kept[(P * PASS + s) / U][(P * PASS + s) % U][i] = t < n ? x : ri4{};
+      }
   }
   __device__ __forceinline__ void load(Held& h, int block, int turn) const {
     const int step = first_step + turn * U;
@@ -368,14 +415,18 @@ struct Rows {
               ri4, __builtin_amdgcn_raw_buffer_load_b128(r, step + u < end_step ? off : kRaggedMasked, u * 64, 0));
       }
       if constexpr (Fm::BLOCKS) {
-        // The scales of four steps are 16 bytes of a row, four for each step, and a
-        // lane's the one of its 32 codes.
+        // The scales of four steps are 16 bytes of a row (of two, 8), four for each step,
+        // and a lane's the one of its 32 codes.
         const auto q = ragged_rsrc(scales[b] + row * scale_ld + step * 4, kRaggedMasked);
         const int at = in * static_cast<int>(scale_ld);
         if (U == 4 && whole) {
           const ri4 w = __builtin_bit_cast(ri4, __builtin_amdgcn_raw_buffer_load_b128(q, at, 0, 0));
 #pragma unroll
           for (int u = 0; u < U; ++u) h.s[u][b] = w[u & 3];
+        } else if (U == 2 && whole) {
+          const ri2 w = __builtin_bit_cast(ri2, __builtin_amdgcn_raw_buffer_load_b64(q, at, 0, 0));
+#pragma unroll
+          for (int u = 0; u < U; ++u) h.s[u][b] = w[u & 1];
         } else {
 #pragma unroll
           for (int u = 0; u < U; ++u)
@@ -413,13 +464,15 @@ struct Rows {
       }
   }
   // What whole steps of 64 bytes leave of the rows: nothing past them is read, and
-  // what is missing counts as zero.  Where weights and values have one type and rows
-  // are 16 bytes or more, the 16 bytes that end with them are loaded with the block's
-  // first turn and shifted down; else all of it waits for the turns.
+  // what is missing counts as zero.  Where weights are not narrow and rows are 16 bytes
+  // or more, the 16 bytes that end with them are loaded with the block's first turn and
+  // shifted down (values too, but for pairs, whose rows are filled up); else all of it
+  // waits for the turns.
+  static constexpr bool RESTS = Fm::SAME || Fm::HALVES;
   struct Rest {
-    ri4 w[NB], x;
+    ri4 w[NB], x[Fm::HALVES ? 2 : 1];
   };
-  __device__ __forceinline__ bool ahead_of_rest() const { return Fm::SAME && row_bytes >= 16; }
+  __device__ __forceinline__ bool ahead_of_rest() const { return RESTS && row_bytes >= 16; }
   __device__ __forceinline__ void load_rest(Rest& h, int block) const {
     const int at = full * 64 + lane / 16 * 16, n = row_bytes - at, back = n > 0 && n < 16 ? 16 - n : 0;
 #pragma unroll
@@ -429,16 +482,26 @@ struct Rows {
           ri4, __builtin_amdgcn_raw_buffer_load_b128(ragged_rsrc(rows[b] + row * ld, kRaggedMasked),
                                                      n > 0 ? lane_row(row) * static_cast<int>(ld) + at - back : kRaggedMasked, 0, 0));
     }
-    h.x = __builtin_bit_cast(
-        ri4, __builtin_amdgcn_raw_buffer_load_b128(ragged_rsrc(values, kRaggedMasked),
-                                                   n > 0 && x_off != kRaggedMasked ? x_off + at - back : kRaggedMasked, 0, 0));
+    const auto v = ragged_rsrc(values, kRaggedMasked);
+    const bool some = n > 0 && x_off != kRaggedMasked;
+    if constexpr (Fm::HALVES) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        h.x[k] = __builtin_bit_cast(
+            ri4, __builtin_amdgcn_raw_buffer_load_b128(v, some ? x_off + 2 * at + 16 * k : kRaggedMasked, 0, 0));
+    } else {
+      h.x[0] = __builtin_bit_cast(
+          ri4, __builtin_amdgcn_raw_buffer_load_b128(v, some ? x_off + at - back : kRaggedMasked, 0, 0));
+    }
   }
   __device__ __forceinline__ void multiply_rest(rf4 (&acc)[NB], const Rest& h) const {
     const int n = row_bytes - (full * 64 + lane / 16 * 16), back = n > 0 && n < 16 ? 16 - n : 0;
     auto down = [&](const ri4& v) { return __builtin_bit_cast(ri4, __builtin_bit_cast(unsigned __int128, v) >> (8 * back)); };
-    const ri4 x = down(h.x);
 #pragma unroll
-    for (int b = 0; b < NB; ++b) ragged_mma<XE, 16>(acc[b], down(h.w[b]), x);
+    for (int b = 0; b < NB; ++b) {
+      if constexpr (Fm::HALVES) layer_mma_pairs<WE>(acc[b], down(h.w[b]), h.x);
+      else ragged_mma<XE, 16>(acc[b], down(h.w[b]), down(h.x[0]));
+    }
   }
   __device__ __forceinline__ void multiply_tail(rf4 (&acc)[NB], int block) const {
     const int at = full * 64 + lane / 16 * 16, n = row_bytes - at;  // valid bytes from here
@@ -480,6 +543,13 @@ struct Rows {
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
         x[i] = ri4{};
+        if constexpr (Fm::PAIR) {  // rows are filled up to whole pieces
+          const int step = first + m * 8;
+          x[i] = __builtin_bit_cast(
+              ri4, __builtin_amdgcn_raw_buffer_load_b128(
+                       v, x_off == kRaggedMasked || step >= steps ? kRaggedMasked : x_off + step * Fm::XS + 16 * i, 0, 0));
+          continue;
+        }
 #pragma unroll
         for (int k = 0; k < EACH; ++k) {
           const int step = first + m * 8 + i * EACH + k;
@@ -494,6 +564,7 @@ struct Rows {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         if constexpr (Fm::SAME) ragged_mma<XE, 16>(acc[b], w[b], x[0]);
+        else if constexpr (Fm::HALVES) layer_mma_pairs<WE>(acc[b], w[b], x);
         else layer_mma_8<XE, WE>(acc[b], w[b][0], w[b][1], x, 0, scale[b]);
         w[b] = Fm::BLOCKS ? ri4{w[b][1], w[b][2], w[b][3], 0} : ri4{w[b][2], w[b][3], 0, 0};
       }
@@ -516,12 +587,12 @@ struct Rows {
     rf4 acc[NB] = {};
     Rest rest;
     auto begin = [&](int block) {
-      if constexpr (Fm::SAME)
+      if constexpr (RESTS)
         if (tail && ahead_of_rest()) load_rest(rest, block);
     };
     auto done = [&](int block) {
       if (tail) {
-        if constexpr (Fm::SAME) {
+        if constexpr (RESTS) {
           if (ahead_of_rest()) multiply_rest(acc, rest);
           else multiply_tail(acc, block);
         } else {
@@ -594,6 +665,22 @@ __device__ __forceinline__ void put(char* p, long long i, float v) {
   else reinterpret_cast<_Float16*>(p)[i] = static_cast<_Float16>(v);
 }
 
+// Value i of a row of h.
+template <int HE>
+__device__ __forceinline__ void put_hidden(char* p, long long i, float v) {
+  if constexpr (HE == kElemF32) {
+    reinterpret_cast<float*>(p)[i] = v;
+  } else {
+    // The nearest bf16, or, where that is infinite and v is not, the one below; what is left rounds again.
+    float top = static_cast<float>(static_cast<__bf16>(v));
+    if (__builtin_fabsf(top) == __builtin_inff())
+      top = __builtin_bit_cast(float, __builtin_bit_cast(unsigned, v) & 0xFFFF0000u);
+    __bf16* const q = reinterpret_cast<__bf16*>(p) + (i / 8) * 16 + i % 8;
+    q[0] = static_cast<__bf16>(top);
+    q[8] = static_cast<__bf16>(v == top ? 0.0f : v - top);
+  }
+}
+
 // Products that another workgroup adds up: stored and loaded past the caches that
 // belong to one die (fences in their place write back, or empty, all of an L2: 4 us
 // and more).
@@ -619,24 +706,30 @@ __device__ __forceinline__ void meet_in_lds() {
 
 // ---------------------------------------------------------------------------
 // Values that stay in registers: U steps and at most MOST turns of them for a wave, so
-// U MOST XV pieces of 16 bytes of each token's, at most 16, or 8 that take more room
-// once they are split.
-template <int XE, int WE>
+// U MOST XV pieces of 16 bytes of each token's, at most 16, or 8 that take more room once
+// they are split.  WIDE: pairs of which 16 are not enough, up to 32.
+template <int XE, int WE, bool WIDE = false>
 struct Kept {
-  static constexpr int XV = Format<XE, WE>::XV, PARTS = Format<XE, WE>::PARTS, PIECES = PARTS == 1 ? 16 : 8;
-  static constexpr int U = PIECES / XV < 4 ? PIECES / XV : PARTS == 1 ? 4 : 2, MOST = PIECES / (U * XV);
+  static constexpr int XV = Format<XE, WE>::XV;
+  static constexpr int PIECES = WIDE ? 32 : Format<XE, WE>::PARTS == 1 || XE == kElemPair ? 16 : 8;
+  static constexpr int U = PIECES / XV < 4 ? PIECES / XV : WIDE || PIECES < 16 ? 2 : 4, MOST = PIECES / (U * XV);
+  static constexpr int ROOM = 16 * 64 * (PIECES < 16 ? PIECES : 16);  // bytes of a wave's LDS
 };
 
-// One of the two products.
-template <int XE, int WE, bool IN>
+// One of the two products.  TYPE: the tokens'.  WIDE: the second one of hidden widths
+// that need 32 pieces of a token's values in a wave's registers, a kernel of its own, for
+// with those in reach the others spill.
+template <int TYPE, int WE, bool IN, bool WIDE = false>
 __global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
+  constexpr int XE = IN ? TYPE : kHidden<TYPE>;
   using Fm = Format<XE, WE>;
-  constexpr int XV = Fm::XV, U = Kept<XE, WE>::U, MOST = Kept<XE, WE>::MOST;
+  using Keep = Kept<XE, WE, WIDE>;
+  constexpr int XV = Fm::XV, U = Keep::U, MOST = Keep::MOST;
   // Values that do not: as many steps as registers hold.
-  constexpr int STEP_REGS = 8 + 4 * XV, U0 = STEP_REGS <= 16 ? 4 : STEP_REGS <= 32 ? 2 : 1;
+  constexpr int STEP_REGS = 8 + 4 * XV, U0 = STEP_REGS <= (Fm::PAIR ? 12 : 16) ? 4 : STEP_REGS <= 32 ? 2 : 1;
   __shared__ union {
-    char values[kWaves][16 * MOST * U * Fm::STEP * Fm::XS];
+    char values[kWaves][Keep::ROOM];
     float sums[2][kWaves][2][16][kRows + 1];
     struct {
       short pair[kLayerPairs];  // of a choice: the pair that holds its products, or -1
@@ -751,9 +844,17 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) 
                                : pair * static_cast<int>(p.ldh);
       if constexpr (R::KEPT) {
         const rlds_t room = (rlds_t)&lds.values[wave][0];
-        r.send_values(room, n, list, IN ? p.top : 1, IN ? p.ldx : p.ldh);
+        const int choices = IN ? p.top : 1;
+        const long long ldx = IN ? p.ldx : p.ldh;
+        r.send_values(room, 0, n, list, choices, ldx);
         r.load_second(second, lo, hi);
-        r.keep_values(room, n);
+        r.template keep_values<0>(room, n);
+        if constexpr (R::PASSES == 2) {
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the first pass is read
+          r.send_values(room, 1, n, list, choices, ldx);
+          asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+          r.template keep_values<1>(room, n);
+        }
         meet_in_lds();  // sums may take their place
       } else {
         r.load(held, lo, 0);
@@ -775,11 +876,18 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) 
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             const int out = gate ? base * 16 + row : base * 32 + b * 16 + row;
-            if (out >= wide) break;
+            if constexpr (IN && kHidden<TYPE> == kElemPair) {
+              if (out >= wide) {
+                if (out < (wide + 7) / 8 * 8) put_hidden<kElemPair>(p.h + to * p.ldh, out, 0.0f);
+                continue;
+              }
+            } else {
+              if (out >= wide) break;
+            }
             if constexpr (WE == kElemI8) v[b] *= row_scale[gate ? b * wide + out : out];
             if constexpr (!IN) publish(p.z + to * p.ldz + out, v[b]);
-            else if (!gate) put<XE>(p.h + to * p.ldh, out, silu(v[b]));
-            else if (b == 1) put<XE>(p.h + to * p.ldh, out, silu(v[0]) * v[1]);
+            else if (!gate) put_hidden<kHidden<TYPE>>(p.h + to * p.ldh, out, silu(v[b]));
+            else if (b == 1) put_hidden<kHidden<TYPE>>(p.h + to * p.ldh, out, silu(v[0]) * v[1]);
           }
         }
       });
@@ -788,10 +896,20 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) 
     using std::integral_constant;
     const int turns = (depth / Fm::STEP + U * sharers - 1) / (U * sharers);
     const integral_constant<int, U> kept_steps;
-    if (turns > MOST) work(integral_constant<int, U0>{}, integral_constant<int, 0>{});
-    else if (MOST == 1 || turns <= 1) work(kept_steps, integral_constant<int, 1>{});
-    else if (MOST == 2 || turns <= 2) work(kept_steps, integral_constant<int, MOST >= 2 ? 2 : 1>{});
-    else work(kept_steps, integral_constant<int, MOST >= 4 ? 4 : 1>{});
+    auto keep = [&] {
+      if (MOST == 1 || turns <= 1) work(kept_steps, integral_constant<int, 1>{});
+      else if (MOST == 2 || turns <= 2) work(kept_steps, integral_constant<int, MOST >= 2 ? 2 : 1>{});
+      else work(kept_steps, integral_constant<int, MOST >= 4 ? 4 : 1>{});
+    };
+    if constexpr (WIDE) {
+      if (turns > MOST) work(integral_constant<int, U0>{}, integral_constant<int, 0>{});
+      else work(kept_steps, integral_constant<int, MOST>{});
+    } else if constexpr (XE == kElemPair) {
+      keep();  // or it would be WIDE
+    } else {
+      if (turns > MOST) work(integral_constant<int, U0>{}, integral_constant<int, 0>{});
+      else keep();
+    }
     turn_of_list ^= 1;
   }
 
@@ -861,8 +979,8 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) 
           for (int i = 0; i < 4; ++i) {
             if (col[k] + i >= wide) break;
             const long long at = token[k] * p.ldy + col[k] + i;
-            if (XE == kElemF32 || p.out32) put<kElemF32>(p.y, at, y[k][i]);
-            else put<XE>(p.y, at, y[k][i]);
+            if (TYPE == kElemF32 || p.out32) put<kElemF32>(p.y, at, y[k][i]);
+            else put<TYPE>(p.y, at, y[k][i]);
           }
         }
       }
@@ -875,14 +993,21 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) 
 // The second product where few experts are used: a workgroup takes 16 columns of y
 // for all tokens, its waves divide the used experts' rows, end to end, and what each
 // finds for a token it adds up in LDS.  No workgroup waits for another's products
-// (one token, 2 of 16 experts, 4096 by 2048: the layer takes 27 us so in bf16 and 16
+// (one token, 2 of 16 experts, 4096 by 2048: the layer takes 28 us so in bf16 and 17
 // in 4 bits, 31 and 20 with the kernel above); with more experts than waves each wave
 // has too many short pieces (8 bits, 2048 by 1024, 16 tokens, 4 choices of 32: 70 us
-// and 54).
+// and 54).  What a workgroup reads grows with the hidden width, by all tokens' values
+// as well, and narrow outputs leave units idle: several tokens come here where T F F <=
+// 6000 D, D up to a unit's columns (2 of 8 experts, 4096 by 2048: 4 tokens in bf16 69 us
+// and 72 above, 16 in 4 bits 45 and 38; 2048 by 4096: one token in bf16 36 and 38, two 52
+// and 49; 2048 by 2048: 4 tokens 52 and 48; 1024 by 512: 8 in 4 bits 17 and 20; 8192 by
+// 1024: 8 in bf16 87 and 83).
 constexpr int kDirectTokens = 16, kDirectExperts = kWaves;
-template <int XE, int WE>
+constexpr double kDirectWidths = 6000;
+template <int TYPE, int WE>
 __global__ __launch_bounds__(kThreads, 2) void expert_out_kernel(const LayerArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
+  constexpr int XE = kHidden<TYPE>;
   using Fm = Format<XE, WE>;
   constexpr int STEP_REGS = 4 + 4 * Fm::XV, U = STEP_REGS <= 8 ? 8 : STEP_REGS <= 16 ? 4 : STEP_REGS <= 24 ? 2 : 1;
   using R = Rows<XE, WE, U, 0, 1>;
@@ -947,8 +1072,8 @@ __global__ __launch_bounds__(kThreads, 2) void expert_out_kernel(const LayerArgs
     float y = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) y += sums[w][t][i % kRows];
-    if (XE == kElemF32 || p.out32) put<kElemF32>(p.y, t * p.ldy + col, y);
-    else put<XE>(p.y, t * p.ldy + col, y);
+    if (TYPE == kElemF32 || p.out32) put<kElemF32>(p.y, t * p.ldy + col, y);
+    else put<TYPE>(p.y, t * p.ldy + col, y);
   }
 #endif
 }
@@ -961,24 +1086,31 @@ hipError_t launch_tokens(const LayerArgs& args, hipStream_t s) {
   a.few = pairs <= kFewPairs && slots <= kFewExperts;
   // Rows beside each other where few waves hold the reduction's values and there are
   // rows for two blocks a workgroup all the same.
-  auto sets = [&](int depth, int wide, int per) {
-    const int steps = depth / Format<XE, WE>::STEP, hold = Kept<XE, WE>::U * Kept<XE, WE>::MOST;
+  auto sets = [&](int hold, int depth, int wide, int per) {  // hold: steps that a wave can keep
+    const int steps = depth / Format<XE, WE>::STEP;
     int n = 1;
     while (n < 4 && steps * 2 * n <= hold * kWaves &&
            static_cast<long long>(wide) * slots >= 2LL * kGroups * per * 2 * n)
       n *= 2;
     return n;
   };
-  a.sets_in = sets(a.D, a.F, a.gated ? 16 : 32);
-  a.sets_out = sets(a.F, a.D, 32);
+  using In = Kept<XE, WE>;
+  using Out = Kept<kHidden<XE>, WE>;
+  constexpr int kInSteps = In::U * In::MOST, kOutSteps = Out::U * Out::MOST;
+  a.sets_in = sets(kInSteps, a.D, a.F, a.gated ? 16 : 32);
+  a.sets_out = sets(kOutSteps, a.F, a.D, 32);
   const hipError_t err = hipLaunchKernel(reinterpret_cast<const void*>(&expert_kernel<XE, WE, true>), dim3(kGroups),
                                          dim3(kThreads), values, 0, s);
   if (err != hipSuccess) return err;
-  if (a.few && a.T <= kDirectTokens && slots <= kDirectExperts)
+  const bool narrow = static_cast<double>(a.T) * a.F * a.F <= kDirectWidths * std::min(a.D, kRows * kGroups);
+  if (a.few && slots <= kDirectExperts && (a.T == 1 || (a.T <= kDirectTokens && narrow)))
     return hipLaunchKernel(reinterpret_cast<const void*>(&expert_out_kernel<XE, WE>),
                            dim3((static_cast<unsigned>(a.D) + kRows - 1) / kRows), dim3(kThreads), values, 0, s);
-  return hipLaunchKernel(reinterpret_cast<const void*>(&expert_kernel<XE, WE, false>), dim3(kGroups), dim3(kThreads),
-                         values, 0, s);
+  const void* out = reinterpret_cast<const void*>(&expert_kernel<XE, WE, false>);
+  if constexpr (kHidden<XE> == kElemPair)
+    if (a.F / Format<XE, WE>::STEP > kOutSteps * kWaves)
+      out = reinterpret_cast<const void*>(&expert_kernel<XE, WE, false, true>);
+  return hipLaunchKernel(out, dim3(kGroups), dim3(kThreads), values, 0, s);
 }
 
 template <int XE>

@@ -13,7 +13,7 @@ struct LayerArgs {
   const char* w_out;   // experts of D rows of F
   const void* scale_in;   // 8-bit weights: floats, a row each; 4-bit: bytes, a block each
   const void* scale_out;
-  char* h;        // workspace: T * top rows of F, of x's type, ldh apart,
+  char* h;        // workspace: T * top rows of F values of 32 bits, ldh apart (16-bit x: pairs, rows of a multiple of 8),
   float* z;       // T * top rows of D, ldz apart,
   int* finished;  // and how often each 32 columns of those are done
   char* y;

@@ -36,7 +36,7 @@ struct LayerRoom {
   long long h_row, z_row, z, counters, all;  // bytes
   LayerRoom(int type, long long T, long long D, long long F, long long top) {
     const auto lines = [](long long n) { return (n + kLine - 1) / kLine * kLine; };
-    h_row = lines(F * elem_size(type));
+    h_row = lines(4 * (type == kElemF32 ? F : (F + 7) / 8 * 8));
     z_row = lines(4 * D);
     z = T * top * h_row;
     counters = z + T * top * z_row;

@@ -77,8 +77,9 @@ int64_t rms_norm_grad_workspace(int64_t M, int64_t K); /* -1 for sizes out of ra
  * row (scale_in experts x 2 F or F, scale_out experts x D), as quantize_rows writes
  * them; 5: microscaled 4-bit floats (leading dimensions and strides in bytes, scales
  * tight, a byte for each block of 32), as quantize_mx4 writes them.  Else the scales
- * are NULL.  Products are exact for 8 and 4 bits, sums 32-bit floats; h is rounded to
- * `type` once.  Only the weights of experts that are named are read.
+ * are NULL.  Products are exact for 8 and 4 bits, sums 32-bit floats; h is held in 32 bits:
+ * a float, or for 16-bit types a sum of two bfloat16, which is off by at most 2^-17 of
+ * it and has a float's range.  Only the weights of experts that are named are read.
  * The workspace holds expert_layer_workspace(type, T, D, F, top) bytes, aligned to 16.
  * -1 type  -2 weights  -3 out_type  -4 gated not 0 or 1  -5 T  -6 D  -7 F negative
  * -8 experts < 1  -9 top < 1  -10 X  -12 ids  -13 share  -14 W_in  -17 scale_in  -18 W_out

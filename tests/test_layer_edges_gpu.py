@@ -1,0 +1,115 @@
+"""Where the norm, its gradient and the layer of experts leave the ordinary range:
+sums and products that pass 32 bits, hidden values that pass 16, scale bytes at the
+ends, rows of the longest kinds.  Bounds count roundings, as in the files whose
+references are used here.
+"""
+import pytest
+import torch
+
+import fp32_gemm_amd as fg
+from test_expert_layer_gpu import HALF_STEP, TINY, make_weights
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+# Hidden values of 16-bit tokens are sums of two bfloat16: the first leaves at most half
+# a step, 2^-8 of the value's power of two, and the second half a step of that, 2^-17.
+HELD = {F32: 2.0 ** -24, BF16: 2.0 ** -17, F16: 2.0 ** -17}
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def layer_reference(x, ids, share, w_in, w_out, gated, held, scaled):
+    """y in 64 bits and how far a result may be off before its own rounding, as in
+    test_expert_layer_gpu, with hidden values that are off by `held` of themselves."""
+    x, share = x.double(), share.double()
+    y, off = torch.zeros(x.shape[0], w_out.shape[1], dtype=torch.float64, device="cuda"), 0
+    off = torch.zeros_like(y)
+    step, F, deep = 2.0 ** -24, w_out.shape[2], w_in.shape[2]
+    for t in range(x.shape[0]):
+        for j in range(ids.shape[1]):
+            e = int(ids[t, j])
+            if not 0 <= e < w_in.shape[0]:
+                continue
+            u = w_in[e] @ x[t]
+            du = (2 * (deep + 4) + 2 * scaled) * step * (w_in[e].abs() @ x[t].abs())
+            a, da = (u[:F], du[:F]) if gated else (u, du)
+            h = a * torch.sigmoid(a)
+            dh = 1.1 * da + 8 * step * h.abs()
+            if gated:
+                dh = dh * (u[F:].abs() + du[F:]) + h.abs() * du[F:]
+                h = h * u[F:]
+                dh = dh + step * h.abs()
+            dh = dh + held * (h.abs() + dh) + 2.0 ** -133
+            y[t] += share[t, j] * (w_out[e] @ h)
+            # Products of two parts of a value by up to two of a weight: up to 4 F sums.
+            off[t] += share[t, j].abs() * (w_out[e].abs() @ dh + (2 * (4 * F + 4) + 2 * scaled + 24) * step * (w_out[e].abs() @ (h.abs() + dh)))
+    return y, off
+
+
+@pytest.mark.parametrize("kind", ["same", "int8", "mx4"])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("E,T,top,D,F", [(3, 1, 2, 64, 64), (8, 16, 2, 96, 200), (5, 3, 2, 40, 77), (4, 20, 2, 70, 129), (12, 9, 3, 64, 7),
+                                         (2, 2, 1, 33, 2500), (2, 30, 1, 33, 2500), (3, 18, 1, 96, 1030), (24, 12, 2, 520, 96)])
+def test_hidden_values_keep_their_bits(dtype, kind, E, T, top, D, F):
+    # Results in 32 bits show how the values between the two products were held.
+    g = gen(E + F)
+    for gated in (True, False):
+        x = torch.randn(T, D, device="cuda", generator=g).to(dtype)
+        w_in, s_in, v_in = make_weights(g, kind, E, 2 * F if gated else F, D, dtype)
+        w_out, s_out, v_out = make_weights(g, kind, E, D, F, dtype)
+        ids = torch.stack([torch.randperm(E, device="cuda", generator=g)[:top] for _ in range(T)]).to(torch.int32)
+        share = torch.rand(T, top, device="cuda", generator=g)
+        y = torch.empty(T, D, device="cuda")
+        fg.expert_layer(x, ids, share, w_in, w_out, y, s_in, s_out, gated=gated)
+        want, off = layer_reference(x, ids, share, v_in, v_out, gated, HELD[dtype], kind == "int8")
+        assert ((y.double() - want).abs() <= off + 2.0 ** -24 * (want.abs() + off) + TINY[F32]).all()
+
+
+@pytest.mark.parametrize("kind", ["same", "int8", "mx4"])
+@pytest.mark.parametrize("E,T", [(2, 3), (12, 30)])
+def test_hidden_values_past_16_bits(kind, E, T):
+    # u * silu(u) passes 65504, the largest of float16, and the result does not.
+    g = gen(T)
+    D, F = 64, 40
+    x = torch.randn(T, D, device="cuda", generator=g).half() * 40
+    w_in, s_in, v_in = make_weights(g, kind, E, 2 * F, D, F16)
+    if kind == "same":
+        w_in, v_in = w_in * 16, v_in * 16
+    elif kind == "int8":
+        s_in, v_in = s_in * 16, v_in * 16
+    else:
+        s_in, v_in = s_in + 4, v_in * 16
+    w_out, s_out, v_out = make_weights(g, kind, E, D, F, F16)
+    if kind == "same":
+        w_out = w_out * 2.0 ** -8
+        v_out = w_out.double()
+    elif kind == "int8":
+        s_out, v_out = s_out * 2.0 ** -8, v_out * 2.0 ** -8
+    else:
+        s_out, v_out = s_out - 8, v_out * 2.0 ** -8
+    ids = torch.randint(0, E, (T, 1), device="cuda", generator=g, dtype=torch.int32)
+    share = torch.rand(T, 1, device="cuda", generator=g)
+    u = torch.stack([v_in[int(e)] @ row for e, row in zip(ids[:, 0], x.double())])
+    assert (torch.nn.functional.silu(u[:, :F]) * u[:, F:]).abs().amax(1).min() > 70000
+    y = torch.empty(T, D, dtype=F16, device="cuda")
+    fg.expert_layer(x, ids, share, w_in, w_out, y, s_in, s_out)
+    want, off = layer_reference(x, ids, share, v_in, v_out, True, HELD[F16], kind == "int8")
+    assert want.abs().max() < 60000
+    assert ((y.double() - want).abs() <= off + HALF_STEP[F16] * (want.abs() + off) + TINY[F16]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("E,T", [(2, 3), (12, 30)])
+def test_infinite_hidden_values(dtype, E, T):
+    # Weights of one sign, zeros of the lower bits among them: infinite sums, not NaN.
+    x = torch.ones(T, 64, device="cuda", dtype=dtype)
+    x[0, 5] = float("inf")
+    w_in = torch.ones(E, 16, 64, device="cuda", dtype=dtype)
+    w_out = (1 + torch.arange(16, device="cuda") / 1024).to(dtype).expand(E, 64, 16).contiguous()
+    y = torch.empty_like(x)
+    ids = torch.arange(T, device="cuda", dtype=torch.int32)[:, None] % E
+    fg.expert_layer(x, ids, torch.ones(T, 1, device="cuda"), w_in, w_out, y, gated=False)
+    assert (y[0] == float("inf")).all() and torch.isfinite(y[1:]).all()
