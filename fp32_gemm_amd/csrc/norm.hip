@@ -6,7 +6,8 @@
 //   dx = s (g - n mean(g n)) + dh,  dw = sum over rows of dy n,  g = dy w, n = h s
 //
 // Sums of squares, s and the largest |v| are held in 64 bits, so that no row of
-// finite numbers overflows and codes are those of the exact quotients.  The largest
+// finite numbers overflows and codes are those of the exact quotients.  h is a sum in 32
+// bits, and one in 64 in rows where it is infinite in 32.  The largest
 // |v| is looked for in 32 bits first; only the 16-byte pieces that may hold it, and
 // codes next to a tie, are computed again in 64.
 #include "norm.hpp"
@@ -179,7 +180,7 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_kernel
   using P = Piece<ELEM>;
   using W = Weights<ELEM, W32>;
   constexpr int ES = elem_size(ELEM), PER = P::PER;
-  __shared__ double room[2][THREADS / 64][2];
+  __shared__ double room[3][THREADS / 64][2];
   const int in = threadIdx.x % THREADS;
   const long long block = static_cast<long long>(blockIdx.y) * kNormBlocks + blockIdx.x;
   const long long row = block * ROWS + threadIdx.x / THREADS;
@@ -252,6 +253,25 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_kernel
     top = bad == 0.0f ? largest : __builtin_inff();
   }
   over_row<Add, Larger, THREADS>(sum, top, room[0]);
+  // Where x + r has passed 32 bits somewhere in the row, or is no number, the thread's
+  // values one by one, from memory again: the registers are for the other rows.
+  const bool past = __builtin_amdgcn_readfirstlane(r != nullptr && !(sum < __builtin_inf()));
+  auto one_by_one = [&](auto with) {
+#pragma unroll 1
+    for (int c = in; c < pieces; c += THREADS)
+#pragma unroll 1
+      for (int i = 0; i < PER; ++i) with(static_cast<long long>(c) * PER + i);
+    if (one) with(last);
+  };
+  if (past) {
+    sum = 0;
+    one_by_one([&](long long i) {
+      const double d = static_cast<double>(element<ELEM>(x, i)) + static_cast<double>(element<ELEM>(r, i));
+      sum = __builtin_fma(d, d, sum);
+    });
+    double none = 0;
+    over_row<Add, Larger, THREADS>(sum, none, room[1]);
+  }
   if constexpr (CODES) {
     // |v| in 32 bits is off by at most 2 * 2^-24 of itself, so the largest lies within
     // 2^-21 of the largest found.  Where that is tiny or no number, all are looked at.
@@ -277,7 +297,7 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_kernel
     }
     if (wrong != 0.0) exact = __builtin_inf();
     double none = 0;
-    over_row<Add, Larger, THREADS>(none, exact, room[1]);
+    over_row<Add, Larger, THREADS>(none, exact, room[2]);
     top = exact;
   }
   const double s = inverse_root(__builtin_fma(sum, p.inv_k, static_cast<double>(p.eps)));
@@ -290,7 +310,16 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_kernel
     if (in == 0) p.scale[row] = top == __builtin_inf() ? __builtin_nanf("") : static_cast<float>(top / 127.0 * s);
 
   char* const h = p.h ? p.h + row * p.ldh * ES : nullptr;
-  char* const y = p.y ? p.y + row * p.ldy * (p.out32 ? 4 : ES) : nullptr;
+  char* y = p.y ? p.y + row * p.ldy * (p.out32 ? 4 : ES) : nullptr;
+  if (past && y) {  // before H takes the place of x or r
+    one_by_one([&](long long i) {
+      const double d = static_cast<double>(element<ELEM>(x, i)) + static_cast<double>(element<ELEM>(r, i));
+      const float v = static_cast<float>(d * s) * W::one(p.w, i);
+      if (ELEM != kElemF32 && p.out32) reinterpret_cast<float*>(y)[i] = v;
+      else set_element<ELEM>(y, i, v);
+    });
+    y = nullptr;
+  }
   signed char* const q = CODES ? p.q + row * p.ldq : nullptr;
   // The inverse's estimate, after two steps of Newton's method.
   double inv64 = CODES ? __builtin_amdgcn_rcp(top) : 0.0;

@@ -113,3 +113,57 @@ def test_infinite_hidden_values(dtype, E, T):
     ids = torch.arange(T, device="cuda", dtype=torch.int32)[:, None] % E
     fg.expert_layer(x, ids, torch.ones(T, 1, device="cuda"), w_in, w_out, y, gated=False)
     assert (y[0] == float("inf")).all() and torch.isfinite(y[1:]).all()
+
+
+def norm_reference(x, r, w, eps):
+    """y, scales and codes in 64 bits, from the sum that is not rounded."""
+    h = x.double() + r.double()
+    s = (h.square().mean(1, keepdim=True) + eps).rsqrt()
+    v = h if w is None else h * w.double()
+    top = v.abs().amax(1, keepdim=True)
+    q = torch.round(v * 127 / torch.where(top > 0, top, 1.0))
+    return v * s, (top / 127 * s)[:, 0], q.to(torch.int8)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,K", [(5, 1), (5, 96), (5, 3001), (600, 2100), (5, 40000), (4100, 1500), (300, 9000)])
+def test_norm_of_sums_past_32_bits(dtype, M, K):
+    # X + R passes the largest float where neither does: Y, scale and codes are made from
+    # the sum itself, and H alone is infinite.
+    g = gen(K)
+    x = torch.randn(M, K, device="cuda", generator=g)
+    r = torch.randn(M, K, device="cuda", generator=g)
+    for row, factor in ((0, 1.0), (1, -1.0), (3, 0.9)):
+        x[row], r[row] = x[row].clamp(-1.5, 1.5) * 1e38, r[row].clamp(-1.5, 1.5) * 1e38
+        x[row, K // 2], r[row, K // 2] = factor * 3.3e38, factor * 2e38
+    x[4], r[4] = 3e38, 3e38
+    x, r = x.to(dtype), r.to(dtype)
+    w = 1 + 0.3 * torch.randn(K, device="cuda", generator=g)
+    for weight in (w, w.to(dtype), None):
+        want, ws, wq = norm_reference(x, r, weight, 1e-6)
+        bound = want.abs() * 5 * 2.0 ** -24 * 1.01 + TINY[F32]
+        y, h = torch.empty(M, K, device="cuda"), torch.empty_like(x)
+        q, scale = torch.empty(M, K, device="cuda", dtype=torch.int8), torch.empty(M, device="cuda")
+        fg.rms_norm(x, weight, y, residual=r, H=h, Q=q, scale=scale)
+        assert ((y.double() - want).abs() <= bound).all()
+        assert ((scale.double() - ws).abs() <= ws * (2 * 2.0 ** -24 + 2.0 ** -40)).all()
+        assert torch.equal(q, wq)
+        assert torch.equal(h, (x.float() + r.float()).to(dtype)) and torch.isinf(h[0, K // 2])
+        fg.rms_norm(x, weight, y.fill_(0), residual=r)
+        assert ((y.double() - want).abs() <= bound).all()
+        a = r.clone()  # H in the residual's place, nothing else in 32 bits
+        fg.rms_norm(x, weight, residual=a, H=a, Q=q.fill_(0), scale=scale.fill_(0))
+        assert torch.equal(q, wq) and torch.equal(a, h)
+        assert ((scale.double() - ws).abs() <= ws * (2 * 2.0 ** -24 + 2.0 ** -40)).all()
+
+
+@pytest.mark.parametrize("K", [70, 3000, 20000])
+def test_sums_of_infinities_are_no_numbers(K):
+    x, r = torch.ones(4, K, device="cuda"), torch.ones(4, K, device="cuda")
+    x[0, 3], r[1, K - 1], x[2, 5], r[2, 5] = float("inf"), float("-inf"), float("inf"), float("-inf")
+    y, h = torch.empty_like(x), torch.empty_like(x)
+    q, scale = torch.empty(4, K, device="cuda", dtype=torch.int8), torch.empty(4, device="cuda")
+    fg.rms_norm(x, None, y, residual=r, H=h, Q=q, scale=scale)
+    assert torch.isnan(scale[:3]).all() and (q[:3] == 0).all() and (q[3] == 127).all()
+    assert torch.isnan(y[0, 3]) and (y[0, 4:] == 0).all() and torch.isnan(y[2]).all() and torch.isfinite(y[3]).all()
+    assert torch.equal(h[[0, 1, 3]], (x + r)[[0, 1, 3]]) and torch.isnan(h[2, 5])
