@@ -165,6 +165,7 @@ constexpr float kNearTie = 0x1p-14f;
 constexpr double kTie = 0x1p-40;
 
 constexpr int kNormBlocks = 1 << 23;  // workgroups in x; more rows go on in y
+static_assert(256LL * kNormBlocks < 1LL << 32, "threads that HIP takes in a dimension");
 
 // One row by THREADS threads of a workgroup of 256 or as many, KEEP pieces a thread in
 // registers as they came; longer rows are read again.  H may be x or r itself: a thread has read
@@ -511,13 +512,15 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_grad_k
 // dw: the teams' sums, a column by sixteen threads that take every 16th team, in a
 // fixed order.
 constexpr int kSumColumns = 64, kSumGroups = 16;
+constexpr int kSumBlocks = 1 << 21;  // workgroups in x; more columns go on in y
+static_assert(1LL * kSumBlocks * kSumColumns * kSumGroups < 1LL << 32, "threads that HIP takes in a dimension");
 template <int OUT>
 __global__ __launch_bounds__(kSumColumns* kSumGroups) void sum_partial_kernel(const float* partial, int teams, int K,
                                                                              char* dw) {
 #ifdef __HIP_DEVICE_COMPILE__
   __shared__ float sums[kSumGroups][kSumColumns];
   const int c = threadIdx.x % kSumColumns, g = threadIdx.x / kSumColumns;
-  const long long col = static_cast<long long>(blockIdx.x) * kSumColumns + c;
+  const long long col = (static_cast<long long>(blockIdx.y) * kSumBlocks + blockIdx.x) * kSumColumns + c;
   float sum = 0.0f;
   if (col < K)
 #pragma unroll 8
@@ -623,8 +626,9 @@ hipError_t rms_norm_grad_launch(int type, bool w32, int dw_type, char* dw, const
   const void* const kernel = dw_type == kElemF32    ? reinterpret_cast<const void*>(&sum_partial_kernel<kElemF32>)
                              : dw_type == kElemBF16 ? reinterpret_cast<const void*>(&sum_partial_kernel<kElemBF16>)
                                                     : reinterpret_cast<const void*>(&sum_partial_kernel<kElemF16>);
-  return hipLaunchKernel(kernel, dim3(static_cast<unsigned>((static_cast<long long>(K) + kSumColumns - 1) / kSumColumns)),
-                         dim3(kSumColumns * kSumGroups), values, 0, s);
+  const unsigned blocks = (static_cast<unsigned>(K) + kSumColumns - 1) / kSumColumns;
+  const dim3 grid(blocks < kSumBlocks ? blocks : kSumBlocks, (blocks + kSumBlocks - 1) / kSumBlocks);
+  return hipLaunchKernel(kernel, grid, dim3(kSumColumns * kSumGroups), values, 0, s);
 }
 
 }  // namespace fp32gemm

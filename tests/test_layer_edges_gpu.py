@@ -167,3 +167,31 @@ def test_sums_of_infinities_are_no_numbers(K):
     assert torch.isnan(scale[:3]).all() and (q[:3] == 0).all() and (q[3] == 127).all()
     assert torch.isnan(y[0, 3]) and (y[0, 4:] == 0).all() and torch.isnan(y[2]).all() and torch.isfinite(y[3]).all()
     assert torch.equal(h[[0, 1, 3]], (x + r)[[0, 1, 3]]) and torch.isnan(h[2, 5])
+
+
+@pytest.mark.parametrize("K", [(1 << 27) + 64, (1 << 28) - 63, (1 << 28) + 77])
+def test_gradient_of_the_longest_rows(K):
+    # The weight's sums are a launch of their own, sixteen threads a column: from 2^28
+    # columns on those are 2^32, more than a dimension takes.
+    g = gen(K % 1000)
+    h, dy = (torch.randn(1, K, device="cuda", generator=g).bfloat16() for _ in range(2))
+    dx, dw = torch.empty_like(h), torch.full((K,), 777.0, device="cuda").bfloat16()
+    fg.rms_norm_grad(dy, h, None, dx, dw)
+    h, dy = h.double(), dy.double()
+    s = (h.square().mean() + 1e-6).rsqrt()
+    n = h.mul_(s)
+    want = dy * n
+    off = 9 * 2.0 ** -24 * want.abs()
+    assert ((dw.double() - want).abs() <= 1.01 * off + HALF_STEP[BF16] * (want.abs() + off) + TINY[BF16]).all()
+    mean, size = want.mean(), want.abs().mean()
+    want = s * (dy - n * mean)
+    off = 2.0 ** -24 * (5 * (s * dy).abs() + 8 * s * n.abs() * size)
+    assert ((dx.double() - want).abs() <= 1.01 * off + HALF_STEP[BF16] * (want.abs() + off) + TINY[BF16]).all()
+
+
+@pytest.mark.parametrize("K", [1 << 28, 1 << 30])
+def test_weight_gradient_of_no_rows(K):
+    e = lambda *s: torch.empty(*s, device="cuda", dtype=BF16)  # noqa: E731
+    dw = torch.full((K,), 777.0, device="cuda", dtype=BF16)
+    fg.rms_norm_grad(e(0, K), e(0, K), None, e(0, K), dw)
+    assert not dw.any()
