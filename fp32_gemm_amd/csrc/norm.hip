@@ -114,6 +114,12 @@ __device__ __forceinline__ double last_lane(double v) {
   return __builtin_bit_cast(double, ru2{static_cast<unsigned>(__builtin_amdgcn_readlane(w[0], 63)),
                                         static_cast<unsigned>(__builtin_amdgcn_readlane(w[1], 63))});
 }
+// Alike in all lanes, so not in the vector registers.
+__device__ __forceinline__ double scalar(double v) {
+  const ru2 w = __builtin_bit_cast(ru2, v);
+  return __builtin_bit_cast(double, ru2{static_cast<unsigned>(__builtin_amdgcn_readfirstlane(w[0])),
+                                        static_cast<unsigned>(__builtin_amdgcn_readfirstlane(w[1]))});
+}
 // Both over the THREADS threads of a row, known to all of them.  `room` holds two
 // values a wave; calls that follow one another take rooms in turn.
 template <class F, class G, int THREADS>
@@ -395,16 +401,17 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_kernel
 
 // The gradient: a team of THREADS threads takes every teams-th row, with its sums
 // for dw in registers, P pieces a thread (0: any length, the sums in memory), and
-// leaves them as a row of `partial`.  Memory-bound: bf16 16384 x 4096 with dh 111 us,
+// leaves them as a row of `partial`.  Rows with a g past 32 bits, which s may bring back,
+// are made in 64 bits, one value after another.  Memory-bound: bf16 16384 x 4096 with dh 111 us,
 // 4.9 TB/s, and 5.5 us for the teams' sums.
 template <int ELEM, bool W32, int THREADS, int PIECES>
-__global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_grad_kernel(const NormGradArgs p) {
+__global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS, PIECES == 4 ? 2 : 4) void rms_norm_grad_kernel(const NormGradArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
   using P = Piece<ELEM>;
   using W = Weights<ELEM, W32>;
   constexpr int ES = elem_size(ELEM), PER = P::PER, HELD = PIECES ? PIECES : 1;
   constexpr int TEAMS = THREADS < 256 ? 256 / THREADS : 1;  // of a workgroup
-  __shared__ double room[2][THREADS / 64][2];
+  __shared__ double room[3][THREADS / 64][2];
   const int in = threadIdx.x % THREADS;
   const int team = blockIdx.x * TEAMS + threadIdx.x / THREADS;
   if (team >= p.teams) return;  // uniform in a wave; teams of several waves are whole workgroups
@@ -426,10 +433,13 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_grad_k
     const char* const dh = p.dh ? p.dh + row * p.lddh * ES : nullptr;
     char* const dx = p.dx + row * p.lddx * ES;
     double square = 0, dot = 0;
+    float largest = 0.0f;
     auto take = [&](float a, float b, float wv) {
       const double d = a;
+      const float g = b * wv;
       square = __builtin_fma(d, d, square);
-      dot = __builtin_fma(d, static_cast<double>(b * wv), dot);
+      dot = __builtin_fma(d, static_cast<double>(g), dot);
+      largest = __builtin_fmaxf(largest, __builtin_fabsf(g));
     };
     P kh[HELD], kd[HELD], kr[HELD];
     if constexpr (PIECES) {
@@ -461,8 +471,12 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_grad_k
     const float h1 = one ? element<ELEM>(h, last) : 0.0f, d1 = one ? element<ELEM>(dy, last) : 0.0f;
     const float r1 = one && dh ? element<ELEM>(dh, last) : 0.0f;
     if (one) take(h1, d1, w1);
+    // |n| is at most 2^15, so where no |g| is larger all that follows stays within 32
+    // bits; else the row's sum becomes no number, which its other threads see.
+    if (largest > 0x1p100f) dot = __builtin_nan("");
     over_row<Add, Add, THREADS>(square, dot, room[turn]);
-    const double s64 = inverse_root(__builtin_fma(square, p.inv_k, static_cast<double>(p.eps)));
+    const bool past = __builtin_amdgcn_readfirstlane(!(__builtin_fabs(dot) < __builtin_inf()));
+    const double s64 = scalar(inverse_root(__builtin_fma(square, p.inv_k, static_cast<double>(p.eps))));
     const Factor s(s64);
     const float mean = static_cast<float>(dot * p.inv_k * s64);
     auto grad = [&](float a, float b, float r, float wv, float& sums) {
@@ -474,7 +488,7 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_grad_k
       float v[PER];
 #pragma unroll
       for (int i = 0; i < PER; ++i) v[i] = grad(a[i], b[i], r[i], wv.at(i), sums[i]);
-      P::store(dx, c, v);
+      if (!past) P::store(dx, c, v);
     };
     if constexpr (PIECES) {
 #pragma unroll
@@ -495,7 +509,34 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_grad_k
         if (at) __builtin_memcpy(at, sums, PER * 4);
       }
     }
-    if (one) set_element<ELEM>(dx, last, grad(h1, d1, r1, w1, dw1));
+    if (one) {
+      const float v = grad(h1, d1, r1, w1, dw1);
+      if (!past) set_element<ELEM>(dx, last, v);
+    }
+    if (past) {  // g or what it is made of passes 32 bits, or is no number: in 64, one by one, from memory
+      int first = in;
+      asm("" : "+v"(first));  // nothing of this is made ready, in registers, for the other rows
+      auto one_by_one = [&](auto with) {
+#pragma unroll 1
+        for (int c = first; c < pieces; c += THREADS)
+#pragma unroll 1
+          for (int i = 0; i < PER; ++i) with(static_cast<long long>(c) * PER + i);
+        if (first < rest) with(static_cast<long long>(pieces) * PER + first);
+      };
+      auto product = [&](long long i) {
+        return static_cast<double>(element<ELEM>(dy, i)) * static_cast<double>(W::one(p.w, i));
+      };
+      double none = 0;
+      dot = 0;
+      one_by_one([&](long long i) { dot = __builtin_fma(static_cast<double>(element<ELEM>(h, i)), product(i), dot); });
+      over_row<Add, Add, THREADS>(none, dot, room[2]);
+      const double middle = dot * p.inv_k * s64;
+      one_by_one([&](long long i) {
+        const double n = static_cast<double>(element<ELEM>(h, i)) * s64;
+        const float v = static_cast<float>(__builtin_fma(-n, middle, product(i)) * s64);
+        set_element<ELEM>(dx, i, dh ? v + element<ELEM>(dh, i) : v);
+      });
+    }
   }
   if (part) {
     if constexpr (PIECES)

@@ -195,3 +195,72 @@ def test_weight_gradient_of_no_rows(K):
     dw = torch.full((K,), 777.0, device="cuda", dtype=BF16)
     fg.rms_norm_grad(e(0, K), e(0, K), None, e(0, K), dw)
     assert not dw.any()
+
+
+def gradient_reference(dy, h, w, dh):
+    """dX, how far it may be off before its own rounding, dweight and its bound, as in test_norm_gpu."""
+    h, dy = h.double(), dy.double()
+    s = (h.square().mean(1, keepdim=True) + 1e-6).rsqrt()
+    g = dy if w is None else dy * w.double()
+    n = h * s
+    dx = s * (g - n * (g * n).mean(1, keepdim=True))
+    size = 2.0 ** -24 * (5 * (s * g).abs() + 8 * s * n.abs() * (g * n).abs().mean(1, keepdim=True))
+    if dh is not None:
+        dx = dx + dh.double()
+        size = size + 2.0 ** -24 * dx.abs()
+    dw = (dy * n).sum(0)
+    return dx, size, dw, (h.shape[0] + 8) * 2.0 ** -24 * (dy * n).abs().sum(0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,K", [(5, 1), (5, 70), (5, 1000), (5, 3001), (700, 5000), (5, 12000), (5, 20000)])
+def test_gradient_of_products_past_32_bits(dtype, M, K):
+    # dY * weight passes the largest float, and the norm's factor brings it back.
+    g = gen(K + 1)
+    h, dy, dh = (torch.randn(M, K, device="cuda", generator=g) for _ in range(3))
+    for row, factor in ((0, 1e37), (2, 2e36), (3, 1e36)):  # the last: the products stay below, their sums do not
+        h[row] *= 1e30
+        dy[row] *= factor
+    h[:, K // 2], dy[:, K // 2] = h[:, K // 2] * 2 + h[:, K // 2].sign(), dy[:, K // 2] * 3
+    h, dy, dh = h.to(dtype), dy.to(dtype), dh.to(dtype)
+    w = 200 * (1 + 0.3 * torch.randn(K, device="cuda", generator=g))
+    for weight, more in ((w, dh), (w.to(dtype), None)):
+        dx, dw = torch.empty_like(h), torch.empty(K, device="cuda")
+        want, size, want_w, size_w = gradient_reference(dy, h, weight, more)
+        assert want.abs().max() < 1e30 and (size_w * 2.0 ** 24 / (M + 8)).max() < torch.finfo(F32).max  # sums of magnitudes
+        bound = 1.01 * size + HALF_STEP[dtype] * (want.abs() + size) + TINY[dtype]
+        fg.rms_norm_grad(dy, h, weight, dx, dw, residual_grad=more)
+        assert ((dx.double() - want).abs() <= bound).all()
+        assert ((dw.double() - want_w).abs() <= 1.01 * size_w + HALF_STEP[F32] * (want_w.abs() + size_w) + TINY[F32]).all()
+        for place in ("dY", "dH"):
+            a = (dy if place == "dY" else dh).clone()
+            fg.rms_norm_grad(a if place == "dY" else dy, h, weight, a, residual_grad=None if more is None else a if place == "dH" else more)
+            if place == "dY" or more is not None:
+                assert torch.equal(a, dx)
+
+
+@pytest.mark.parametrize("K", [500, 3001, 20000])
+def test_gradient_of_means_past_32_bits(K):
+    # Every product is finite, and their mean times a large value of the row is not.
+    g = gen(K + 5)
+    h = torch.randn(3, K, device="cuda", generator=g) * 1e25
+    h[1, 7] = 2e26
+    dy = h.sign() * 3.2e38
+    dx = torch.empty_like(h)
+    fg.rms_norm_grad(dy, h, None, dx)
+    want, size, _, _ = gradient_reference(dy, h, None, None)
+    assert ((dx.double() - want).abs() <= 1.01 * size + HALF_STEP[F32] * (want.abs() + size)).all()
+
+
+@pytest.mark.parametrize("K", [70, 3000, 20000])
+def test_gradient_of_values_that_are_no_numbers(K):
+    g = gen(K + 6)
+    h, dy, dh = (torch.randn(5, K, device="cuda", generator=g) for _ in range(3))
+    clean = torch.empty_like(h)
+    fg.rms_norm_grad(dy, h, None, clean, residual_grad=dh)
+    dh[0, 3], dy[1, 5], h[3, K - 1] = float("inf"), float("nan"), float("nan")
+    dx, dw = torch.empty_like(h), torch.empty(K, device="cuda")
+    fg.rms_norm_grad(dy, h, None, dx, dw, residual_grad=dh)
+    assert dx[0, 3] == float("inf") and torch.equal(dx[0, 4:], clean[0, 4:])
+    assert torch.isnan(dx[1]).all() and torch.isnan(dx[3]).all() and torch.equal(dx[[2, 4]], clean[[2, 4]])
+    assert torch.isnan(dw).all()
