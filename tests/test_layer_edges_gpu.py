@@ -264,3 +264,123 @@ def test_gradient_of_values_that_are_no_numbers(K):
     assert dx[0, 3] == float("inf") and torch.equal(dx[0, 4:], clean[0, 4:])
     assert torch.isnan(dx[1]).all() and torch.isnan(dx[3]).all() and torch.equal(dx[[2, 4]], clean[[2, 4]])
     assert torch.isnan(dw).all()
+
+
+@pytest.mark.parametrize("dtype,K", [(BF16, 16400), (BF16, 16501), (F16, 17003), (F32, 8300), (F32, 8203)])
+@pytest.mark.parametrize("M", [513, 1100])
+def test_weight_gradient_of_many_long_rows(dtype, K, M):
+    # Rows too long for registers, and more of them than teams: a team adds to its sums in memory.
+    from test_norm_gpu import check_gradient
+    g = gen(M + K)
+    h, dy, dh = (torch.randn(M, K, device="cuda", generator=g).to(dtype) for _ in range(3))
+    w = 1 + 0.3 * torch.randn(K, device="cuda", generator=g)
+    room = torch.full((fg.layers.rms_norm_grad_workspace(M, K),), 0xFF, dtype=torch.uint8, device="cuda")  # NaN
+    for weight, into, more in ((w.to(dtype), dtype, dh), (w, F32, None)):
+        dx, dw = torch.empty_like(h), torch.empty(K, device="cuda", dtype=into)
+        fg.rms_norm_grad(dy, h, weight, dx, dw, residual_grad=more, workspace=room)
+        check_gradient(dy, h, weight, more, 1e-6, dx, dw)
+        a, again = dy.clone(), torch.empty_like(dw)
+        fg.rms_norm_grad(a, h, weight, a, again, residual_grad=more, workspace=room)
+        assert torch.equal(a, dx) and torch.equal(again, dw)
+
+
+def block_values(q, s):
+    """What codes stand for under their scale bytes, in 64 bits: 255 is no number."""
+    table = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device="cuda")
+    v = torch.cat([table, -table])[torch.stack((q & 15, q >> 4), -1).long()].flatten(-2)
+    step = torch.where(s == 255, float("nan"), torch.ldexp(torch.ones((), dtype=torch.float64, device="cuda"), s.double() - 127))
+    return v * step.repeat_interleave(32, -1)[..., :v.shape[-1]]
+
+
+FORMS = [(2, 3), (12, 30)]  # experts, tokens: the direct second product, and the other
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("byte", [0, 1, 2, 30, 250, 252])
+@pytest.mark.parametrize("E,T", FORMS)
+@pytest.mark.parametrize("D,F", [(256, 128), (200, 77)])
+def test_scale_bytes_of_the_first_weights(dtype, byte, E, T, D, F):
+    # Every block has its scale near an end of the range, tokens bring the sums back: each
+    # product is a normal float, or a subnormal bfloat16 times one.
+    g = gen(byte + D)
+    power = 127 - byte
+    x = (torch.randn(T, D, device="cuda", generator=g) * 2.0 ** max(min(power, 120), -100)).to(dtype)
+    w_in = torch.randint(0, 256, (E, F, (D + 1) // 2), dtype=torch.uint8, device="cuda", generator=g)
+    s_in = torch.full((E, F, (D + 31) // 32), byte, dtype=torch.uint8, device="cuda")
+    v_in = block_values(w_in, s_in)[..., :D]
+    w_out, s_out, v_out = make_weights(g, "mx4", E, D, F, dtype)
+    ids = torch.randint(0, E, (T, 1), device="cuda", generator=g, dtype=torch.int32)
+    share = torch.rand(T, 1, device="cuda", generator=g)
+    y = torch.empty(T, D, device="cuda")
+    fg.expert_layer(x, ids, share, w_in, w_out, y, s_in, s_out, gated=False)
+    want, off = layer_reference(x, ids, share, v_in, v_out, False, HELD[dtype], False)
+    assert want.abs().amax() > 2.0 ** -10 and torch.isfinite(y).all()
+    assert ((y.double() - want).abs() <= off + 2.0 ** -24 * (want.abs() + off) + TINY[F32]).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("byte", [0, 1, 2, 30, 250, 252])
+@pytest.mark.parametrize("E,T", FORMS)
+@pytest.mark.parametrize("D,F", [(64, 256), (40, 205)])
+def test_scale_bytes_of_the_second_weights(dtype, byte, E, T, D, F):
+    # Shares bring the results back.
+    g = gen(byte + F)
+    x = torch.randn(T, D, device="cuda", generator=g).to(dtype)
+    w_in, s_in, v_in = make_weights(g, "mx4", E, F, D, dtype)
+    w_out = torch.randint(0, 256, (E, D, (F + 1) // 2), dtype=torch.uint8, device="cuda", generator=g)
+    s_out = torch.full((E, D, (F + 31) // 32), byte, dtype=torch.uint8, device="cuda")
+    if byte >= 250:  # sums of one expert stay finite: a block of each row, the others zero
+        w_out[:, :, 16:] = 0
+        w_out &= 0x33
+    v_out = block_values(w_out, s_out)[..., :F]
+    ids = torch.randint(0, E, (T, 1), device="cuda", generator=g, dtype=torch.int32)
+    share = torch.rand(T, 1, device="cuda", generator=g) * 2.0 ** max(min(127 - byte, 110), -120)
+    if byte >= 250:
+        w_in, s_in = w_in, s_in - 8
+        v_in = v_in * 2.0 ** -8
+    y = torch.empty(T, D, device="cuda")
+    fg.expert_layer(x, ids, share, w_in, w_out, y, s_in, s_out, gated=False)
+    want, off = layer_reference(x, ids, share, v_in, v_out, False, HELD[dtype], False)
+    # Sums of numbers near the smallest lose their last bits: a subnormal's half step each.
+    lost = (4 * F + 4) * 2.0 ** -149 * share.double()
+    assert want.abs().amax() > 0 and torch.isfinite(y).all()
+    assert ((y.double() - want).abs() <= off + lost + 2.0 ** -24 * (want.abs() + off) + TINY[F32]).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("E,T", FORMS)
+@pytest.mark.parametrize("D,F", [(256, 128), (200, 77)])
+def test_blocks_that_are_no_numbers(dtype, E, T, D, F):
+    # Scale byte 255, codes zero: its row of W_in makes the token's results NaN, its row of
+    # W_out one column.  Blocks of zeros, as quantize_mx4 writes them, change nothing.
+    g = gen(D + E)
+    x = torch.randn(T, D, device="cuda", generator=g).to(dtype)
+    w_in, s_in, v_in = make_weights(g, "mx4", E, F, D, dtype)
+    w_out, s_out, v_out = make_weights(g, "mx4", E, D, F, dtype)
+    ids = (torch.arange(T, device="cuda", dtype=torch.int32) % E)[:, None].contiguous()
+    share = torch.rand(T, 1, device="cuda", generator=g) + 0.5
+    def spoil(w, s, v, e, row, block, byte):
+        w[e, row, 16 * block:16 * block + 16], s[e, row, block] = 0, byte
+        v[e, row, 32 * block:32 * block + 32] = 0
+    last_d, last_f = (D - 1) // 32, (F - 1) // 32
+    for e in range(E):
+        spoil(w_in, s_in, v_in, e, 1, 0, 0), spoil(w_in, s_in, v_in, e, F - 1, last_d, 0)
+        spoil(w_out, s_out, v_out, e, 2, 0, 0), spoil(w_out, s_out, v_out, e, D - 1, last_f, 0)
+    for block in (0, last_f):
+        w, s = w_out.clone(), s_out.clone()
+        spoil(w, s, v_out.clone(), 0, 5, block, 255)
+        y = torch.empty(T, D, device="cuda")
+        fg.expert_layer(x, ids, share, w_in, w, y, s_in, s, gated=False)
+        want, off = layer_reference(x, ids, share, v_in, v_out, False, HELD[dtype], False)
+        hit = torch.zeros(T, D, dtype=torch.bool, device="cuda")
+        hit[ids[:, 0] == 0, 5] = True
+        assert torch.isnan(y[hit]).all()
+        assert ((y.double() - want).abs() <= off + 2.0 ** -24 * (want.abs() + off) + TINY[F32])[~hit].all()
+    for block in (0, last_d):
+        w, s = w_in.clone(), s_in.clone()
+        spoil(w, s, v_in.clone(), 0, 3, block, 255)
+        y = torch.empty(T, D, device="cuda")
+        fg.expert_layer(x, ids, share, w, w_out, y, s, s_out, gated=False)
+        assert torch.isnan(y[ids[:, 0] == 0]).all()
+        rest = ids[:, 0] != 0
+        assert ((y.double() - want).abs() <= off + 2.0 ** -24 * (want.abs() + off) + TINY[F32])[rest].all()
