@@ -3,8 +3,8 @@
 //   h[t, j] = silu(G_e x_t) * (U_e x_t)   (or silu(U_e x_t)),   e = ids[t, j]
 //   y[t] = sum_j share[t, j] D_e h[t, j]
 //
-// What bounds it is reading the chosen experts' weights, once each.  Both kernels
-// multiply an expert's rows by the gathered values of up to 16 of its tokens.  There
+// What bounds it is reading the chosen experts' weights, once for each 16 of their
+// tokens.  Both kernels multiply an expert's rows by the gathered values of up to 16.  There
 // is one workgroup a compute unit; each takes an equal run of all the rows that are to
 // be multiplied.  Its eight waves divide the reduction, of 32 rows at a time, or, where
 // it is short, two or four times as many rows as well; they add up in LDS in a fixed
@@ -50,24 +50,33 @@ __device__ __forceinline__ int lanes_below(unsigned long long m) {
 // What the ids say: the experts that any token names, in the order of the pairs
 // (token, choice) that name them first, and each one's pairs.  A token that names
 // an expert more than once counts once; ids out of range name nothing.  An expert
-// whose pairs are more than 16 is taken once for each 16: the entries below.  There
-// are two ways to them.
+// whose pairs are more than 16 is taken once for each 16, its weights read as often: the
+// entries below, none of which is empty.  There are two ways to them.
 
 // Up to 128 pairs that name up to 32 experts: every wave finds them by itself, two
 // pairs a lane and a few instructions for each expert.
 constexpr int kFewPairs = 128, kFewExperts = 32;
 struct FewPairs {
-  int id[2];  // of pairs lane and 64 + lane; -1: none
-  int top;
+  int id[2];  // of pairs lane and 64 + lane; -1: none, or an earlier choice of the token is the same
 
   __device__ __forceinline__ void init(const LayerArgs& p, int lane) {
-    top = p.top;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int i = 64 * k + lane;
       const int e = i < p.T * p.top ? p.ids[i] : -1;
       id[k] = e >= 0 && e < p.experts ? e : -1;
     }
+    bool again[2] = {};
+    for (int d = 1; d < p.top; ++d) {  // the token's other choices; all lanes fetch
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int i = 64 * k + lane;
+        const int before0 = __shfl(id[0], i - d & 63), before1 = __shfl(id[1], i - d & 63);
+        again[k] |= d <= i % p.top && (i - d < 64 ? before0 : before1) == id[k];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) id[k] = again[k] ? -1 : id[k];
   }
   // Calls visit(expert, entries) for one expert after another until it says no.
   template <class F>
@@ -108,15 +117,10 @@ struct FewPairs {
     int n = -first;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int i = 64 * k + lane, j = i % top;
-      bool mine = id[k] == e;
-      for (int d = 1; d < top; ++d) {  // the token's other choices; all lanes fetch
-        const int before0 = __shfl(id[0], i - d & 63), before1 = __shfl(id[1], i - d & 63);
-        if (d <= j && (i - d < 64 ? before0 : before1) == e) mine = false;
-      }
+      const bool mine = id[k] == e;
       const unsigned long long m = __ballot(mine);
       const int at = n + lanes_below(m);
-      if (mine && at >= 0 && at < 16) list[at] = static_cast<short>(i);
+      if (mine && at >= 0 && at < 16) list[at] = static_cast<short>(64 * k + lane);
       n += __builtin_popcountll(m);
     }
     __builtin_amdgcn_wave_barrier();
@@ -1029,7 +1033,6 @@ __global__ __launch_bounds__(kThreads, 2) void expert_out_kernel(const LayerArgs
     few.entry(v, e, set);
     e = __builtin_amdgcn_readfirstlane(e);
     const int n = __builtin_amdgcn_readfirstlane(few.list_pairs(e, 16 * set, list, lane));
-    if (n == 0) continue;  // the rest of e's pairs were a token's second ones: `list` holds nothing
     const int pair = list[lane % 16 < n ? lane % 16 : 0], token = pair / p.top;
     R r;
     r.lane = lane;

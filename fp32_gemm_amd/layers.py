@@ -84,7 +84,8 @@ def rms_norm_grad_workspace(M: int, K: int) -> int:
 def expert_layer(X, ids, share, W_in, W_out, Y, scale_in=None, scale_out=None, gated=True, workspace=None,
                  stream=None):
     """Y[t] <- sum over j of share[t, j] * W_out[e] @ h, e = ids[t, j], for up to 64 tokens
-    (and 512 choices in all), in two kernels that read each named expert's weights once.
+    (and 512 choices in all), in two kernels that read each named expert's weights once for each
+    16 of its tokens.
 
     h = silu(u[:F]) * u[F:] with u = W_in[e] @ X[t] and W_in E x 2F x D, or, without
     ``gated``, h = silu(u) and W_in E x F x D; W_out is E x D x F.  X is T x D, float32,
