@@ -229,8 +229,9 @@ struct Format {
   static constexpr int PER = WE == kElemM4 ? 32 : 16 / elem_size(WE);  // weights of 16 bytes
   static constexpr int STEP = 4 * PER;                                  // of a step
   static constexpr int XV = PER * XS / 16;                              // 16-byte pieces of values for them
-  // Narrow weights become bf16, exactly; values become a sum of one, two or
-  // three bf16, exactly too, and are multiplied one after another.
+  // Narrow weights become bf16, exactly but for 4-bit ones past 2^128; values become a sum
+  // of one, two or three bf16, exactly down to 2^-133, the least bf16, and are multiplied
+  // one after another.
   static constexpr int PARTS = SAME ? 1 : XE == kElemBF16 ? 1 : XE == kElemF16 || PAIR ? 2 : 3;
   static constexpr int MMAS = SAME ? 1 : PER / 8;
 };

@@ -36,7 +36,9 @@ struct Plan {
 // What a tile costs, in microseconds as measured: a slice of 128 bytes of the
 // reduction on a busy compute unit and on one that holds no other tile, and a
 // tile's start and end with results of 2 and of 4 bytes.  32-bit floats take
-// four times the matrix instructions a slice; 4-bit codes as many as 8-bit ones.
+// four times the matrix instructions a slice.  8-bit and 4-bit operands are planned by
+// the costs of 16-bit ones, which those of 4 bits do not quite follow: at 8192 x 8192 x
+// 8192 a slice of the widest tile takes some 1.8.
 struct TileCost { double busy, alone, ends2, ends4; };
 constexpr TileCost kCost16[kShapes] = {{1.4, 1.4, 7.2, 8.5}, {.50, .64, 2.0, 2.5}, {.54, .52, 2.3, 3},
                                        {.19, .28, .9, .9},    {.135, .2, .5, .5},   {.09, .11, .5, .5}};

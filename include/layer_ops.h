@@ -34,16 +34,17 @@ extern "C" {
  * and the same rows in 8 bits, as quantize_rows would bring Y to them before it is
  * rounded: scale[r] = max_k |Y[r,k]| / 127, Q[r,k] = the integer nearest to 127 * Y[r,k] /
  * max_k |Y[r,k]|, ties to even.  A row whose values are all zero gets codes 0, a row
- * with a value that is not finite scale NaN and codes 0.
+ * with a value that is not finite scale NaN and codes 0.  A sum of finite values past the
+ * largest float makes H infinite, and neither Y nor Q.
  * X, R and H are M x K of `type`; R may be NULL (H = X).  H, Y and Q may each be NULL
  * when not wanted, but not Y and Q both.  Y and Q are made from the sum before it is
  * rounded to H.  weight: K values of weight_type, `type` or GEMM_F32, or NULL for
  * ones.  out_type: Y's, `type` or GEMM_F32.  H may be X or R itself, with the same
  * leading dimension; no other operands may overlap an output.
  * -1 type  -2 weight_type  -3 out_type  -4 M  -5 K negative  -6 eps negative or
- * not a number  -7 X NULL while not empty  -15 Y and Q both NULL  -16 Q NULL with scale
- * while not empty  -18 scale NULL with Q  -8 ldx  -10 ldr  -13 ldh  -15 ldy  -17 ldq smaller than a row (of an operand
- * that is given) */
+ * not a number  -7 X NULL while not empty  -8 ldx  -10 ldr  -13 ldh smaller than a row (of
+ * an operand that is given)  -15 ldy so, or Y and Q both NULL  -16 Q NULL with scale while
+ * not empty  -17 ldq smaller than a row  -18 scale NULL with Q */
 int rms_norm(int32_t type, int32_t weight_type, int32_t out_type, int64_t M, int64_t K, float eps,
              const void* X, int64_t ldx, const void* R, int64_t ldr, const void* weight, void* H,
              int64_t ldh, void* Y, int64_t ldy, int8_t* Q, int64_t ldq, float* scale, void* stream);
@@ -77,7 +78,9 @@ int64_t rms_norm_grad_workspace(int64_t M, int64_t K); /* -1 for sizes out of ra
  * row (scale_in experts x 2 F or F, scale_out experts x D), as quantize_rows writes
  * them; 5: microscaled 4-bit floats (leading dimensions and strides in bytes, scales
  * tight, a byte for each block of 32), as quantize_mx4 writes them.  Else the scales
- * are NULL.  Products are exact for 8 and 4 bits, sums 32-bit floats; h is held in 32 bits:
+ * are NULL.  Products are exact, sums 32-bit floats; for 8 and 4 bits, 32-bit values are
+ * sums of three bfloat16 (what lies below 2^-133 is lost), and 4-bit weights are bfloat16
+ * (those past 2^128, of scale bytes 253 and 254, are infinite).  h is held in 32 bits:
  * a float, or for 16-bit types a sum of two bfloat16, which is off by at most 2^-17 of
  * it and has a float's range.  Only the weights of experts that are named are read.
  * The workspace holds expert_layer_workspace(type, T, D, F, top) bytes, aligned to 16.

@@ -384,3 +384,55 @@ def test_blocks_that_are_no_numbers(dtype, E, T, D, F):
         assert torch.isnan(y[ids[:, 0] == 0]).all()
         rest = ids[:, 0] != 0
         assert ((y.double() - want).abs() <= off + 2.0 ** -24 * (want.abs() + off) + TINY[F32])[rest].all()
+
+
+@pytest.mark.parametrize("kind", ["int8", "mx4"])
+@pytest.mark.parametrize("power", [-100, -112, -120, -126])
+@pytest.mark.parametrize("E,T", FORMS)
+def test_tiny_floats_times_narrow_weights(kind, power, E, T):
+    # 32-bit tokens are sums of three bfloat16, which end at 2^-133: what is below is lost,
+    # once a value.  Scales and shares bring the results back.
+    g = gen(-power)
+    D, F = 96, 40
+    x = torch.randn(T, D, device="cuda", generator=g) * 2.0 ** power
+    w_in, s_in, v_in = make_weights(g, kind, E, F, D, F32)
+    up = min(-power, 110)
+    s_in = s_in * 2.0 ** up if kind == "int8" else s_in + up
+    v_in = v_in * 2.0 ** up
+    w_out, s_out, v_out = make_weights(g, kind, E, D, F, F32)
+    ids = torch.randint(0, E, (T, 1), device="cuda", generator=g, dtype=torch.int32)
+    share = torch.rand(T, 1, device="cuda", generator=g)
+    y = torch.empty(T, D, device="cuda")
+    fg.expert_layer(x, ids, share, w_in, w_out, y, s_in, s_out, gated=False)
+    want, off = layer_reference(x, ids, share, v_in, v_out, False, HELD[F32], kind == "int8")
+    # A sum over D is off by 2^-133 |w| for each value, and by a subnormal's half step for
+    # each addition; silu's slope is below 1.1.  So is h, where it falls below 2^-110.
+    for t in range(T):
+        e = int(ids[t, 0])
+        lost = v_in[e].abs().sum(1) * 2.0 ** -133 + (4 * D + 4) * 2.0 ** -149 * 2.0 ** up
+        off[t] += share[t, 0].double() * (v_out[e].abs() @ (1.1 * lost + 2.0 ** -133)) + (4 * F + 4) * 2.0 ** -149
+    assert ((y.double() - want).abs() <= off + 2.0 ** -24 * (want.abs() + off) + TINY[F32]).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("byte,codes", [(253, 0x33), (254, 0x11), (254, 0x77)])
+@pytest.mark.parametrize("E,T", FORMS)
+def test_largest_scale_bytes(dtype, byte, codes, E, T):
+    # Weights are multiplied as bfloat16: past 2^128 they are infinite.
+    g = gen(byte + codes)
+    D, F = 64, 32
+    x = (torch.randn(T, D, device="cuda", generator=g) * 2.0 ** -100).to(dtype)
+    w_in = torch.full((E, F, D // 2), codes, dtype=torch.uint8, device="cuda")
+    s_in = torch.full((E, F, D // 32), byte, dtype=torch.uint8, device="cuda")
+    w_out, s_out, v_out = make_weights(g, "mx4", E, D, F, dtype)
+    v_out = v_out * 2.0 ** -30
+    ids = torch.randint(0, E, (T, 1), device="cuda", generator=g, dtype=torch.int32)
+    share = torch.rand(T, 1, device="cuda", generator=g)
+    y = torch.empty(T, D, device="cuda")
+    fg.expert_layer(x, ids, share, w_in, w_out, y, s_in, s_out - 30, gated=False)
+    if codes == 0x77:
+        assert not torch.isfinite(y).any()
+        return
+    v_in = block_values(w_in, s_in)
+    want, off = layer_reference(x, ids, share, v_in, v_out, False, HELD[dtype], False)
+    assert ((y.double() - want).abs() <= off + 2.0 ** -24 * (want.abs() + off) + TINY[F32]).all()
