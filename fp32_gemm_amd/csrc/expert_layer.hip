@@ -33,8 +33,6 @@
 
 #include "ragged_kernels.hpp"
 
-#include <algorithm>
-
 namespace fp32gemm {
 namespace {
 
@@ -611,7 +609,8 @@ struct Rows {
     if constexpr (KEPT) {
       // The turns of a block, or of two, are written out, so that each knows its
       // registers.  Two are on their way while one is multiplied or its sums are
-      // shared (one: 8 tokens, 2 choices of 32, 4 bits, 4096 by 2048: 52 us for 46).
+      // shared (one: 8 tokens, 2 choices of 32, 4 bits, 4096 by 2048, when it was built:
+      // 52 us for 46).
       constexpr int BLOCKS = Q % 2 ? 2 : 1;
       for (int block = lo; block < hi; block += BLOCKS) {
 #pragma unroll
@@ -721,9 +720,9 @@ struct Kept {
   static constexpr int ROOM = 16 * 64 * (PIECES < 16 ? PIECES : 16);  // bytes of a wave's LDS
 };
 
-// One of the two products.  TYPE: the tokens'.  WIDE: the second one of hidden widths
-// that need 32 pieces of a token's values in a wave's registers, a kernel of its own, for
-// with those in reach the others spill.
+// One of the two products.  TYPE: the tokens'.  WIDE: the second one with up to 32 pieces
+// of a token's values in a wave's registers, a kernel of its own, for with those in reach
+// the others spill.
 template <int TYPE, int WE, bool IN, bool WIDE = false>
 __global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
@@ -773,8 +772,8 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) 
   // This workgroup's units, a block of an entry each; where nothing is used, y alone
   // is left to be written, block by block.  Each entry that a workgroup begins costs
   // it a few microseconds of latency, so the entries get whole workgroups where that
-  // leaves few over (32 experts, 16 tokens, 4 choices, 8 bits, 2048 by 1024: 54 us,
-  // and 63 with units in equal runs whatever the entry).
+  // leaves few over (32 experts, 16 tokens, 4 choices, 8 bits, 2048 by 1024, when it was
+  // built: 54 us, and 63 with units in equal runs whatever the entry).
   const int owners = max(entries, IN ? 0 : 1), group = blockIdx.x;
   const int each = owners > 0 ? kGroups / owners : 0;
   int begin = 0, end = 0;  // fewer than 2^24 in all: 512 entries of 2^15 blocks
@@ -1000,13 +999,13 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(const LayerArgs p) 
 // finds for a token it adds up in LDS.  No workgroup waits for another's products
 // (one token, 2 of 16 experts, 4096 by 2048: the layer takes 28 us so in bf16 and 17
 // in 4 bits, 31 and 20 with the kernel above); with more experts than waves each wave
-// has too many short pieces (8 bits, 2048 by 1024, 16 tokens, 4 choices of 32: 70 us
-// and 54).  What a workgroup reads grows with the hidden width, by all tokens' values
-// as well, and narrow outputs leave units idle: several tokens come here where T F F <=
-// 6000 D, D up to a unit's columns (2 of 8 experts, 4096 by 2048: 4 tokens in bf16 69 us
-// and 72 above, 16 in 4 bits 45 and 38; 2048 by 4096: one token in bf16 36 and 38, two 52
-// and 49; 2048 by 2048: 4 tokens 52 and 48; 1024 by 512: 8 in 4 bits 17 and 20; 8192 by
-// 1024: 8 in bf16 87 and 83).
+// has too many short pieces (8 bits, 2048 by 1024, 16 tokens, 4 choices of 32: 73 us
+// and 59).  What a workgroup reads grows with the hidden width, by all tokens' values
+// as well, narrow outputs leave units idle, and wide ones are more workgroups than
+// units: several tokens come here where T F F <= 6000 D and D <= 4096 (2 of 8 experts,
+// 4096 by 2048: 4 tokens in bf16 69 us and 72 above, 16 in 4 bits 45 and 38; 2048 by 4096:
+// one token in bf16 36 and 38, two 52 and 49; 2048 by 2048: 4 tokens 50 and 47; 1024 by
+// 512: 8 in 4 bits 17 and 20; 8192 by 1024: 8 in bf16 86 and 83).
 constexpr int kDirectTokens = 16, kDirectExperts = kWaves;
 constexpr double kDirectWidths = 6000;
 template <int TYPE, int WE>
@@ -1103,17 +1102,25 @@ hipError_t launch_tokens(const LayerArgs& args, hipStream_t s) {
   constexpr int kInSteps = In::U * In::MOST, kOutSteps = Out::U * Out::MOST;
   a.sets_in = sets(kInSteps, a.D, a.F, a.gated ? 16 : 32);
   a.sets_out = sets(kOutSteps, a.F, a.D, 32);
+  // Hidden widths that need more room, or that in 8 bits have more rows beside each other
+  // with it (64 tokens, 4096 by 2048: 42.5 us for 45; in 4 bits alike).
+  bool wide = false;
+  if constexpr (kHidden<XE> == kElemPair) {
+    using More = Kept<kHidden<XE>, WE, true>;
+    const int more = sets(More::U * More::MOST, a.F, a.D, 32);
+    wide = a.F / Format<XE, WE>::STEP > kOutSteps * kWaves || (WE == kElemI8 && more > a.sets_out);
+    if (wide) a.sets_out = more;
+  }
   const hipError_t err = hipLaunchKernel(reinterpret_cast<const void*>(&expert_kernel<XE, WE, true>), dim3(kGroups),
                                          dim3(kThreads), values, 0, s);
   if (err != hipSuccess) return err;
-  const bool narrow = static_cast<double>(a.T) * a.F * a.F <= kDirectWidths * std::min(a.D, kRows * kGroups);
+  const bool narrow = a.D <= kRows * kGroups && static_cast<double>(a.T) * a.F * a.F <= kDirectWidths * a.D;
   if (a.few && slots <= kDirectExperts && (a.T == 1 || (a.T <= kDirectTokens && narrow)))
     return hipLaunchKernel(reinterpret_cast<const void*>(&expert_out_kernel<XE, WE>),
                            dim3((static_cast<unsigned>(a.D) + kRows - 1) / kRows), dim3(kThreads), values, 0, s);
   const void* out = reinterpret_cast<const void*>(&expert_kernel<XE, WE, false>);
   if constexpr (kHidden<XE> == kElemPair)
-    if (a.F / Format<XE, WE>::STEP > kOutSteps * kWaves)
-      out = reinterpret_cast<const void*>(&expert_kernel<XE, WE, false, true>);
+    if (wide) out = reinterpret_cast<const void*>(&expert_kernel<XE, WE, false, true>);
   return hipLaunchKernel(out, dim3(kGroups), dim3(kThreads), values, 0, s);
 }
 

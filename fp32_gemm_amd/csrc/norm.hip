@@ -586,11 +586,11 @@ template <int ELEM, bool W32>
 hipError_t launch_norm(const NormArgs& args, hipStream_t s) {
   // A wave takes rows of up to two pieces a lane, and where there are rows enough for
   // all waves of up to eight, or four with codes (16384 x 4096, residual and codes:
-  // 111 us with eight, 96 by four waves); longer ones go to four waves, or, where
+  // 115 us with eight, 94 by four waves); longer ones go to four waves, or, where
   // few rows leave the card idle and a row's instructions are what takes time, to eight
-  // or sixteen (bf16 with codes: 1 x 4096 3.8 us, and 4.2 by four waves, 256 x 16384 12.6
-  // and 17.3, but 512 x 8192 14.1 and 12.4; without 1 x 16384 4.4 and 7.8, 512 x 8192 8.7
-  // and 9.9, but 1024 x 8192 15.0 and 13.9).
+  // or sixteen (bf16 with a residual, codes: 1 x 4096 4.5 us, and 4.7 by four waves, 256 x
+  // 16384 12.6 and 15.9, but 512 x 8192 14.1 and 12.0; Y: 1 x 16384 4.7 and 7.2, 512 x 8192
+  // 8.4 and 9.1, but 1024 x 8192 13.6 and 13.0).
   const int pieces = args.K / Piece<ELEM>::PER;
   const bool codes = args.scale != nullptr;
   const bool wave = pieces <= 128 || (pieces <= (codes ? 256 : 512) && args.M >= 4096);

@@ -88,12 +88,12 @@ def expert_layer(X, ids, share, W_in, W_out, Y, scale_in=None, scale_out=None, g
     16 of its tokens.
 
     h = silu(u[:F]) * u[F:] with u = W_in[e] @ X[t] and W_in E x 2F x D, or, without
-    ``gated``, h = silu(u) and W_in E x F x D; W_out is E x D x F.  h is held in 32 bits.  X is T x D, float32,
-    bfloat16 or float16, Y T x D of its type or float32.  ids (int32) and share (float32)
-    are T x top; an id that is no expert's counts for nothing.  The weights have X's
-    type, or are int8 with float32 scales E x rows as :func:`quantize_rows` writes them, or
-    uint8 with scales as :func:`quantize_mx4` writes them.  workspace: uint8,
-    ``layers.expert_layer_workspace(X, ids, F)`` bytes.
+    ``gated``, h = silu(u) and W_in E x F x D; W_out is E x D x F.  h is held in 32 bits.
+    X is T x D, float32, bfloat16 or float16, Y T x D of its type or float32.  ids (int32)
+    and share (float32) are T x top; an id that is no expert's counts for nothing.  The
+    weights have X's type, or are int8 with float32 scales E x rows as
+    :func:`quantize_rows` writes them, or uint8 with scales as :func:`quantize_mx4` writes
+    them.  workspace: uint8, ``layers.expert_layer_workspace(X, ids, F)`` bytes.
     """
     status = _torch_calls.expert_layer(X, ids, share, W_in, W_out, Y, scale_in, scale_out, gated, workspace, stream)
     if status:

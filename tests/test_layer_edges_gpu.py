@@ -52,7 +52,8 @@ def layer_reference(x, ids, share, w_in, w_out, gated, held, scaled):
 @pytest.mark.parametrize("kind", ["same", "int8", "mx4"])
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
 @pytest.mark.parametrize("E,T,top,D,F", [(3, 1, 2, 64, 64), (8, 16, 2, 96, 200), (5, 3, 2, 40, 77), (4, 20, 2, 70, 129), (12, 9, 3, 64, 7),
-                                         (2, 2, 1, 33, 2500), (2, 30, 1, 33, 2500), (3, 18, 1, 96, 1030), (24, 12, 2, 520, 96)])
+                                         (2, 2, 1, 33, 2500), (2, 30, 1, 33, 2500), (3, 18, 1, 96, 1030), (24, 12, 2, 520, 96),
+                                         (16, 20, 2, 2100, 1100), (16, 20, 1, 2056, 2047), (32, 20, 2, 2100, 600)])
 def test_hidden_values_keep_their_bits(dtype, kind, E, T, top, D, F):
     # Results in 32 bits show how the values between the two products were held.
     g = gen(E + F)
