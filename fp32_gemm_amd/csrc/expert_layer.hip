@@ -15,8 +15,8 @@
 // an expert's rows.
 //
 // Measured, for the layer of 4096 by 2048 with a gate: one token, 2 of 16 experts in
-// bf16 28 us (3.6 TB/s over both kernels), 64 tokens, 16 experts in 8 bits 105 us
-// (3.6 TB/s), in bf16 165 us (4.9 TB/s).  The kernels stream 5 TB/s once they are
+// bf16 28 us (3.6 TB/s over both kernels), 64 tokens, 16 experts in 8 bits 107 us
+// (3.6 TB/s), in bf16 165 to 172 us (4.8 TB/s).  The kernels stream 5 TB/s once they are
 // under way; what is left is each kernel's start (launch, ids, first loads: 5 us in
 // which little arrives) and the last sums (3 us, 6 for 64 tokens).
 //
@@ -24,7 +24,7 @@
 // a sum of two bf16, to 2^-17 of itself and with the range of a float.  The matrix
 // instruction takes such parts as they lie (rounded to the tokens' type instead, h was
 // what results were off by, 2.3e-3 for 1.7e-3, and infinite past 65504 in f16; that took
-// 1 us less for one token in bf16, 3 for 64 in 8 bits).
+// 1 us less for one token in bf16, 4 for 64 in 8 bits).
 //
 // The second kernel leaves an expert's products, not yet shared out, for each pair
 // of token and choice; the last workgroup to finish a block of columns adds them up

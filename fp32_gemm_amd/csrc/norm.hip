@@ -402,8 +402,8 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_kernel
 // The gradient: a team of THREADS threads takes every teams-th row, with its sums
 // for dw in registers, P pieces a thread (0: any length, the sums in memory), and
 // leaves them as a row of `partial`.  Rows with a g past 32 bits, which s may bring back,
-// are made in 64 bits, one value after another.  Memory-bound: bf16 16384 x 4096 with dh 111 us,
-// 4.9 TB/s, and 5.5 us for the teams' sums.
+// are made in 64 bits, one value after another.  Memory-bound: bf16 16384 x 4096 with dh 114 us,
+// 4.7 TB/s, and 5.6 us for the teams' sums.
 template <int ELEM, bool W32, int THREADS, int PIECES>
 __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS, PIECES == 4 ? 2 : 4) void rms_norm_grad_kernel(const NormGradArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
@@ -588,9 +588,9 @@ hipError_t launch_norm(const NormArgs& args, hipStream_t s) {
   // all waves of up to eight, or four with codes (16384 x 4096, residual and codes:
   // 115 us with eight, 94 by four waves); longer ones go to four waves, or, where
   // few rows leave the card idle and a row's instructions are what takes time, to eight
-  // or sixteen (bf16 with a residual, codes: 1 x 4096 4.5 us, and 4.7 by four waves, 256 x
-  // 16384 12.6 and 15.9, but 512 x 8192 14.1 and 12.0; Y: 1 x 16384 4.7 and 7.2, 512 x 8192
-  // 8.4 and 9.1, but 1024 x 8192 13.6 and 13.0).
+  // or sixteen (bf16 with a residual, codes: 256 x 8192 7.8 us, and 8.4 by four waves, 256 x
+  // 16384 12.6 and 15.8, but 512 x 8192 14.1 and 11.8; Y: 1 x 16384 4.7 and 7.2, 512 x 8192
+  // 8.5 and 9.2, but 1024 x 8192 13.3 and 12.9).
   const int pieces = args.K / Piece<ELEM>::PER;
   const bool codes = args.scale != nullptr;
   const bool wave = pieces <= 128 || (pieces <= (codes ? 256 : 512) && args.M >= 4096);
